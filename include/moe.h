@@ -80,7 +80,8 @@ MOE_API const char* moe_error_string(int status);
  * moe_dispatch_dedup; 102 the FP8-weight calls; 103 moe_ep_recv_experts and
  * FP8 weights at every batch size; 104 the FP8-activation (W8A8) calls and
  * moe_quantise_rows_e4m3 (the workspace grows by their buffers); 105
- * moe_copy, and the layer calls' y may be pinned host memory. */
+ * moe_copy, and the layer calls' y may be pinned host memory.  The calls that
+ * train the gate came with 105 unchanged: they only add symbols. */
 MOE_API int moe_version(void);
 
 /* Bytes of scratch workspace `ws` that moe_dispatch / moe_ffn / moe_forward
@@ -441,6 +442,138 @@ MOE_API int moe_quantise_rows_e4m3(const moe_bf16* a, int64_t rows, int32_t cols
  * MOE_ERR_INVALID_ARG; overlapping ranges are undefined.  bytes == 0 does
  * nothing. */
 MOE_API int moe_copy(void* dst, const void* src, int64_t bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Training the gate.  The pages describe what an unbalanced gate costs
+ * ("Serving MoE models with expert parallelism on 8xH200", section "Routing
+ * imbalance") but no training; these calls are this library's own, the usual
+ * balance loss and the backward of the layer's gate path:
+ *   moe_router, moe_topk, ..., moe_combine       (the forward step)
+ *   moe_balance_loss                             loss, counts
+ *   moe_combine_bwd                              dy -> dw (and dz)
+ *   moe_gate_bwd                                 dw and the loss -> dlogits
+ *   moe_router_bwd                               dlogits -> dw_g, dbias, dx
+ *   moe_clip_grads                               any gradients, in one list
+ * Every sum has a fixed order: equal inputs give equal bits.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of workspace for moe_balance_loss, moe_gate_bwd and moe_router_bwd of
+ * this shape with up to S sequences (1 .. 65535); 0 if the arguments are
+ * invalid.  256-byte aligned, its first 64 bytes zeroed once, one call at a
+ * time, as moe_workspace_size's. */
+MOE_API size_t moe_workspace_size_bwd(const moe_shape* s, int32_t S);
+
+/* Balance loss and per-expert counts of a batch, in S sequences (or as one).
+ *   logits      [T, E] fp32 in   moe_router's output
+ *   idx         [T, k] int32 in  moe_topk's selections
+ *   token_mask  [T] uint8 in or NULL   0: the token does not count
+ *   seq_offsets [S+1] int32 in or NULL (then S must be 1)  sequence i holds the
+ *               tokens [seq_offsets[i], seq_offsets[i+1]); ascending, in
+ *               [0, T]; empty sequences are allowed, and tokens before the
+ *               first or behind the last one belong to none
+ *   loss        [3] fp32 out     {balance + z, balance, z}
+ *   counts      [S, E] int32 out selections of each expert by the sequence's
+ *               counted tokens
+ *   tokens      [S+2] int32 out  counted tokens N_i of each sequence, then
+ *               their sum N, then the number S' of sequences with N_i > 0
+ *   prob_mean   [S, E] fp32 out or NULL   mean probability of each expert
+ *   ws          moe_workspace_size_bwd(s, S) bytes
+ * A token counts if it lies in a sequence, its mask (if any) is not 0 and its
+ * logits are not all -inf (single -inf logits are experts of probability 0).
+ * With p the softmax of a token's logits and lse their logsumexp, over the
+ * counted tokens,
+ *   balance = balance_coef / S' * sum_i E / (k N_i) * sum_e counts[i,e] prob_mean[i,e]
+ *   z       = z_coef / N * sum_t lse_t^2
+ * (1 / S' and 1 / N over nothing give 0; a coefficient of 0 leaves its term
+ * out).  NaN or +inf in a counted token's logits makes its sequence's results
+ * NaN; uncounted tokens' values are not looked at.  Bad offsets and ids
+ * outside [0, E) are recorded as MOE_ERR_DEVICE_CHECK; such an id is not
+ * counted. */
+MOE_API int moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* token_mask,
+                             const int32_t* seq_offsets, int32_t S, const moe_shape* s,
+                             float balance_coef, float z_coef, float* loss, int32_t* counts,
+                             int32_t* tokens, float* prob_mean, void* ws, void* stream);
+
+/* Gradient of the router logits, from the gates' gradient and the balance loss:
+ *   dlogits[t,e] = sum_j 1[idx[t,j] = e] w[t,j] (dw[t,j] - sum_i w[t,i] dw[t,i])
+ *                + dloss * d(balance + z) / d logits[t,e]
+ * (the selections and counts are constants: the loss reaches the logits
+ * through prob_mean and lse).
+ *   w, dw       [T, k] fp32 in   moe_topk's gates and their gradient; dw NULL
+ *               leaves the first term out (then w and idx may be NULL)
+ *   counts, tokens               moe_balance_loss's outputs for the same logits,
+ *               mask, sequences and coefficients; counts NULL leaves the second
+ *               term out (then logits, tokens and the rest may be NULL)
+ *   dloss       [1] fp32 in or NULL (= 1)   gradient of the loss, on the device
+ *   dlogits     [T, E] fp32 out  every row is written; tokens that do not count
+ *               get the first term alone
+ *   ws          only its error word is used
+ * Ids outside [0, E) are recorded as MOE_ERR_DEVICE_CHECK and skipped. */
+MOE_API int moe_gate_bwd(const float* logits, const int32_t* idx, const float* w, const float* dw,
+                         const uint8_t* token_mask, const int32_t* seq_offsets, int32_t S,
+                         const int32_t* counts, const int32_t* tokens, const moe_shape* s,
+                         float balance_coef, float z_coef, const float* dloss, float* dlogits,
+                         void* ws, void* stream);
+
+/* Backward of moe_combine:
+ *   dw[t,j] = sum_c dy[t,c] z[row_of[t,j],c]       (fp32)
+ *   dz[row_of[t,j],c] = w[t,j] dy[t,c]             (one rounding to bf16)
+ *   dy [T, d] bf16 in; row_of [T, k] int32 in; z [T*k, d] bf16 in (may be NULL
+ *   without dw); w [T, k] fp32 in (may be NULL without dz);
+ *   dw [T, k] fp32 out or NULL; dz [T*k, d] bf16 out or NULL, not both NULL.
+ * A row index outside [0, T*k) gives dw = 0 and no row of dz; rows of dz that
+ * no index names are left as they were. */
+MOE_API int moe_combine_bwd(const moe_bf16* dy, const moe_bf16* z, const int32_t* row_of,
+                            const float* w, const moe_shape* s, float* dw, moe_bf16* dz,
+                            void* stream);
+
+/* Backward of moe_router:
+ *   dw_g[i,e] = sum_t x[t,i] dlogits[t,e];  dbias[e] = sum_t dlogits[t,e]
+ *   dx[t,i] = sum_e dlogits[t,e] w_g[i,e]   (one rounding to bf16)
+ *   x [T, d] bf16 in (may be NULL without dw_g); w_g [d, E] fp32 in (may be
+ *   NULL without dx); dlogits [T, E] fp32 in;
+ *   dw_g [d, E] fp32, dbias [E] fp32, dx [T, d] bf16 out, any of them NULL but
+ *   not all.  Overwritten, not added to (T = 0 gives zeros).
+ *   ws moe_workspace_size_bwd(s, 1) bytes */
+MOE_API int moe_router_bwd(const moe_bf16* x, const float* w_g, const float* dlogits,
+                           const moe_shape* s, float* dw_g, float* dbias, moe_bf16* dx, void* ws,
+                           void* stream);
+
+/* A gradient of a list: n elements, read from data and, scaled, written to
+ * out (out == data: in place; otherwise the two must not overlap).  Both
+ * aligned to their own element only. */
+typedef struct moe_grad {
+  const void* data;  /* device memory; may be NULL if n == 0 */
+  void* out;         /* device memory; NULL where only the norm is asked for */
+  int64_t n;         /* elements, 0 <= n <= 1<<40 */
+  int32_t dtype;     /* of data: MOE_GRAD_FP32 or MOE_GRAD_BF16 */
+  int32_t out_dtype; /* dtype, or MOE_GRAD_FP32 */
+} moe_grad;
+enum { MOE_GRAD_FP32 = 0, MOE_GRAD_BF16 = 1 };
+
+/* Workspace bytes for moe_grad_sumsq and moe_clip_grads over n gradients
+ * (0 <= n <= 65536; 0 if n is invalid); 256-byte aligned, first 64 bytes
+ * zeroed once, one call at a time. */
+MOE_API size_t moe_workspace_size_grads(int32_t n);
+
+/* sumsq[0] = the sum of the squares of all elements (fp64 products and sums,
+ * in a fixed order).  `grads` is a host array of n entries, read before the
+ * call returns; their `out` is not looked at. */
+MOE_API int moe_grad_sumsq(const moe_grad* grads, int32_t n, double* sumsq, void* ws,
+                           void* stream);
+
+/* With norm = sqrt(sumsq[0]) (a device value: moe_grad_sumsq's, or the sum of
+ * those of several ranks) and c = min(1, max_norm / (norm + 1e-6)), or 1 if
+ * norm is not finite: every gradient's out = c * data, rounded once, and
+ * norm_out[0] = norm (fp32, may be NULL).  In place and with c = 1 nothing is
+ * written.  max_norm >= 0; infinity scales nothing. */
+MOE_API int moe_grad_scale(const moe_grad* grads, int32_t n, const double* sumsq,
+                           float max_norm, float* norm_out, void* stream);
+
+/* moe_grad_sumsq and moe_grad_scale in one call: gradients clipped by their
+ * global norm, with no host synchronisation. */
+MOE_API int moe_clip_grads(const moe_grad* grads, int32_t n, float max_norm, float* norm_out,
+                           void* ws, void* stream);
 
 /* Self-test of the failure path every device-side wait uses: launches one
  * kernel that waits on a barrier nothing will ever complete, through the same

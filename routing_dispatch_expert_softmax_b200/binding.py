@@ -34,7 +34,9 @@ EXPORTS = ("moe_error_string", "moe_version", "moe_workspace_size", "moe_router"
            "moe_workspace_size_eplb", "moe_forward_eplb", "moe_dispatch_dedup",
            "moe_ffn_fp8", "moe_forward_fp8", "moe_forward_fp8_staged", "moe_ep_recv_experts",
            "moe_ffn_w8a8", "moe_forward_w8a8", "moe_forward_w8a8_staged",
-           "moe_quantise_rows_e4m3", "moe_copy")
+           "moe_quantise_rows_e4m3", "moe_copy", "moe_workspace_size_bwd", "moe_balance_loss",
+           "moe_gate_bwd", "moe_combine_bwd", "moe_router_bwd", "moe_workspace_size_grads",
+           "moe_grad_sumsq", "moe_grad_scale", "moe_clip_grads")
 
 
 class MoEError(RuntimeError):
@@ -54,6 +56,12 @@ class MoEShape(ctypes.Structure):
     @classmethod
     def from_config(cls, cfg) -> "MoEShape":
         return cls.of(cfg.T, cfg.d, cfg.E, cfg.k, cfg.f, cfg.R)
+
+
+class MoEGrad(ctypes.Structure):
+    """moe_grad: one gradient of a list."""
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -127,6 +135,26 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.moe_quantise_rows_e4m3.argtypes = [_P, ctypes.c_int64, ctypes.c_int32, _P, _P, _P]
     lib.moe_copy.restype = ctypes.c_int
     lib.moe_copy.argtypes = [_P, _P, ctypes.c_int64, _P]
+    _f = ctypes.c_float
+    lib.moe_workspace_size_bwd.restype = ctypes.c_size_t
+    lib.moe_workspace_size_bwd.argtypes = [_S, _i32]
+    lib.moe_balance_loss.restype = ctypes.c_int
+    lib.moe_balance_loss.argtypes = [_P, _P, _P, _P, _i32, _S, _f, _f, _P, _P, _P, _P, _P, _P]
+    lib.moe_gate_bwd.restype = ctypes.c_int
+    lib.moe_gate_bwd.argtypes = [_P, _P, _P, _P, _P, _P, _i32, _P, _P, _S, _f, _f, _P, _P, _P,
+                                 _P]
+    lib.moe_combine_bwd.restype = ctypes.c_int
+    lib.moe_combine_bwd.argtypes = [_P, _P, _P, _P, _S, _P, _P, _P]
+    lib.moe_router_bwd.restype = ctypes.c_int
+    lib.moe_router_bwd.argtypes = [_P, _P, _P, _S, _P, _P, _P, _P, _P]
+    lib.moe_workspace_size_grads.restype = ctypes.c_size_t
+    lib.moe_workspace_size_grads.argtypes = [_i32]
+    lib.moe_grad_sumsq.restype = ctypes.c_int
+    lib.moe_grad_sumsq.argtypes = [_P, _i32, _P, _P, _P]
+    lib.moe_grad_scale.restype = ctypes.c_int
+    lib.moe_grad_scale.argtypes = [_P, _i32, _P, _f, _P, _P]
+    lib.moe_clip_grads.restype = ctypes.c_int
+    lib.moe_clip_grads.argtypes = [_P, _i32, _f, _P, _P, _P]
     _lib = lib
     return lib
 
@@ -463,6 +491,259 @@ def moe_forward_fp8_staged(x, w_g, bias, w13, w13_scale, w2, w2_scale, y, shape:
         _ptr(w2_scale, torch.float32, "w2_scale"), ctypes.byref(shape),
         _ptr(y, torch.bfloat16, "y"), _ptr(ws, torch.uint8, "ws"), arr, _stream(st)),
         "moe_forward_fp8_staged")
+
+
+# ------------------------------------------------------- training the gate
+class _Operands:
+    """The tensors of one call: each is checked (CUDA, dtype, shape,
+    contiguity, the call's one device) and gives its address; ``launch`` runs
+    the call on that device and the stream asked for (default: the device's
+    current one)."""
+
+    __slots__ = ("where", "index")
+
+    def __init__(self, where: str):
+        self.where, self.index = where, None
+
+    def ptr(self, t, dtype, shape, name, optional=False):
+        if t is None:
+            if optional:
+                return None
+            raise TypeError(f"{self.where}: {name} is required")
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{self.where}: {name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{self.where}: {name} must be a CUDA tensor "
+                             "(the library has no CPU path)")
+        if t.dtype != dtype:
+            raise TypeError(f"{self.where}: {name} must be {dtype}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{self.where}: {name} must have shape {tuple(shape)}, "
+                             f"got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{self.where}: {name} must be contiguous")
+        index = t.get_device()
+        if self.index is None:
+            self.index = index
+        elif index != self.index:
+            raise ValueError(f"{self.where}: {name} is on cuda:{index}, other tensors on "
+                             f"cuda:{self.index}")
+        return t.data_ptr()
+
+    def workspace(self, ws, need: int):
+        p = self.ptr(ws, torch.uint8, None, "ws")
+        if ws.numel() < need:
+            raise ValueError(f"{self.where}: ws has {ws.numel()} bytes, needs {need}")
+        return p
+
+    def launch(self, fn, stream, *args):
+        if stream is not None and stream.device_index != self.index:
+            raise ValueError(f"{self.where}: the stream is on cuda:{stream.device_index}, the "
+                             f"tensors on cuda:{self.index}")
+        if self.index == torch.cuda.current_device():
+            status = fn(*args, self._stream(stream))
+        else:
+            with torch.cuda.device(self.index):
+                status = fn(*args, self._stream(stream))
+        if status != MOE_OK:
+            raise MoEError(status, self.where)
+
+    def _stream(self, stream):
+        return (torch.cuda.current_stream(self.index) if stream is None else stream).cuda_stream
+
+
+def moe_workspace_size_bwd(shape: MoEShape, S: int = 1) -> int:
+    return int(load_library().moe_workspace_size_bwd(ctypes.byref(shape), int(S)))
+
+
+def workspace_bwd(shape: MoEShape, S: int = 1, device="cuda") -> torch.Tensor:
+    """A zeroed workspace for moe_balance_loss, moe_gate_bwd and
+    moe_router_bwd of this shape with up to S sequences."""
+    n = moe_workspace_size_bwd(shape, S)
+    if n == 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, "moe_workspace_size_bwd")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _seq_count(where, seq_offsets) -> int:
+    if seq_offsets is None:
+        return 1
+    if not isinstance(seq_offsets, torch.Tensor) or seq_offsets.dim() != 1 or len(seq_offsets) < 2:
+        raise ValueError(f"{where}: seq_offsets must be a tensor of S + 1 >= 2 offsets")
+    return len(seq_offsets) - 1
+
+
+def moe_balance_loss(logits, idx, loss, counts, tokens, shape: MoEShape, ws, balance_coef=1e-2,
+                     z_coef=0.0, token_mask=None, seq_offsets=None, prob_mean=None, stream=None):
+    """Balance and z loss with per-expert counts, over the S sequences of
+    ``seq_offsets`` (int32, S + 1 ascending token offsets) or the whole batch
+    (S = 1).  ``loss`` (3,) receives {balance + z, balance, z}, ``counts``
+    (S, E) and ``tokens`` (S + 2,) what moe_gate_bwd reads again,
+    ``prob_mean`` (S, E), if given, the experts' mean probabilities.
+    ``token_mask`` (T,) uint8: 0 leaves the token out."""
+    o = _Operands("moe_balance_loss")
+    T, E, k = shape.T, shape.E, shape.k
+    S = _seq_count(o.where, seq_offsets)
+    need = moe_workspace_size_bwd(shape, S)
+    args = (o.ptr(logits, torch.float32, (T, E), "logits"),
+            o.ptr(idx, torch.int32, (T, k), "idx"),
+            o.ptr(token_mask, torch.uint8, (T,), "token_mask", True),
+            o.ptr(seq_offsets, torch.int32, None, "seq_offsets", True), S, ctypes.byref(shape),
+            balance_coef, z_coef, o.ptr(loss, torch.float32, (3,), "loss"),
+            o.ptr(counts, torch.int32, (S, E), "counts"),
+            o.ptr(tokens, torch.int32, (S + 2,), "tokens"),
+            o.ptr(prob_mean, torch.float32, (S, E), "prob_mean", True), o.workspace(ws, need))
+    o.launch(load_library().moe_balance_loss, stream, *args)
+
+
+def moe_gate_bwd(logits, idx, dlogits, shape: MoEShape, ws, w=None, dw=None, counts=None,
+                 tokens=None, balance_coef=1e-2, z_coef=0.0, dloss=None, token_mask=None,
+                 seq_offsets=None, stream=None):
+    """Gradient of the router logits: through the gates ``w`` (T, k) from their
+    gradient ``dw``, and of moe_balance_loss from its ``counts`` and
+    ``tokens`` (same logits, mask, sequences and coefficients), times the
+    device scalar ``dloss`` (1,) if given.  Either part may be left out."""
+    o = _Operands("moe_gate_bwd")
+    T, E, k = shape.T, shape.E, shape.k
+    S = _seq_count(o.where, seq_offsets)
+    gates, aux = dw is not None, counts is not None
+    args = (o.ptr(logits, torch.float32, (T, E), "logits", not aux),
+            o.ptr(idx, torch.int32, (T, k), "idx", not gates),
+            o.ptr(w, torch.float32, (T, k), "w", not gates),
+            o.ptr(dw, torch.float32, (T, k), "dw", True),
+            o.ptr(token_mask, torch.uint8, (T,), "token_mask", True),
+            o.ptr(seq_offsets, torch.int32, None, "seq_offsets", True), S,
+            o.ptr(counts, torch.int32, (S, E), "counts", True),
+            o.ptr(tokens, torch.int32, (S + 2,), "tokens", not aux), ctypes.byref(shape),
+            balance_coef, z_coef, o.ptr(dloss, torch.float32, (1,), "dloss", True),
+            o.ptr(dlogits, torch.float32, (T, E), "dlogits"), o.workspace(ws, 64))
+    o.launch(load_library().moe_gate_bwd, stream, *args)
+
+
+def moe_combine_bwd(dy, z, row_of, w, shape: MoEShape, dw=None, dz=None, stream=None):
+    """Backward of moe_combine: ``dw`` (T, k) fp32 from dy and z, ``dz``
+    (T*k, d) bf16 from dy and w; either may be left out (and z or w with it)."""
+    o = _Operands("moe_combine_bwd")
+    T, d, k = shape.T, shape.d, shape.k
+    args = (o.ptr(dy, torch.bfloat16, (T, d), "dy"),
+            o.ptr(z, torch.bfloat16, (T * k, d), "z", dw is None),
+            o.ptr(row_of, torch.int32, (T, k), "row_of"),
+            o.ptr(w, torch.float32, (T, k), "w", dz is None), ctypes.byref(shape),
+            o.ptr(dw, torch.float32, (T, k), "dw", True),
+            o.ptr(dz, torch.bfloat16, (T * k, d), "dz", True))
+    o.launch(load_library().moe_combine_bwd, stream, *args)
+
+
+def moe_router_bwd(x, w_g, dlogits, shape: MoEShape, ws, dw_g=None, dbias=None, dx=None,
+                   stream=None):
+    """Backward of moe_router: ``dw_g`` (d, E) and ``dbias`` (E,) fp32, ``dx``
+    (T, d) bf16; each is optional (x serves dw_g alone, w_g dx alone)."""
+    o = _Operands("moe_router_bwd")
+    T, d, E = shape.T, shape.d, shape.E
+    need = moe_workspace_size_bwd(shape, 1)
+    args = (o.ptr(x, torch.bfloat16, (T, d), "x", dw_g is None),
+            o.ptr(w_g, torch.float32, (d, E), "w_g", dx is None),
+            o.ptr(dlogits, torch.float32, (T, E), "dlogits"), ctypes.byref(shape),
+            o.ptr(dw_g, torch.float32, (d, E), "dw_g", True),
+            o.ptr(dbias, torch.float32, (E,), "dbias", True),
+            o.ptr(dx, torch.bfloat16, (T, d), "dx", True), o.workspace(ws, need))
+    o.launch(load_library().moe_router_bwd, stream, *args)
+
+
+_GRAD_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+class GradList:
+    """A list of gradients (contiguous fp32 or bf16 CUDA tensors of any
+    alignment) for moe_grad_sumsq / moe_grad_scale / moe_clip_grads, kept with
+    its workspace so that a training loop marshals it once.  ``outs``: where
+    the scaled gradients go, tensors of the same element counts, each of its
+    gradient's dtype or fp32; default: in place.  The tensors' addresses are
+    read again at every call; their dtypes and element counts are not.  As
+    with any workspace, calls on one GradList must not run concurrently."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError("GradList: as many outs as grads are needed")
+        if not self.grads:
+            raise ValueError("GradList: no gradients")
+        self.n = len(self.grads)
+        self._entries = (MoEGrad * self.n)()
+        self._seen = None
+        self._refresh()
+        need = int(load_library().moe_workspace_size_grads(self.n))
+        if need == 0:
+            raise MoEError(MOE_ERR_INVALID_ARG, "moe_workspace_size_grads")
+        self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+
+    def _refresh(self):
+        """Checks the tensors and fills the entries, unless no address has
+        changed since the last time."""
+        seen = [t.data_ptr() for t in self.grads]
+        if self.outs is not self.grads:
+            seen += [t.data_ptr() for t in self.outs]
+        if seen == self._seen:
+            return
+        o = _Operands("GradList")
+        for i, (g, out, e) in enumerate(zip(self.grads, self.outs, self._entries)):
+            if not isinstance(g, torch.Tensor) or g.dtype not in _GRAD_TYPES:
+                raise TypeError(f"GradList: gradient {i} must be an fp32 or bf16 tensor")
+            if not isinstance(out, torch.Tensor) or out.dtype not in (g.dtype, torch.float32):
+                raise TypeError(f"GradList: out {i} must be {g.dtype} or torch.float32")
+            if out.numel() != g.numel():
+                raise ValueError(f"GradList: out {i} has {out.numel()} elements, its gradient "
+                                 f"{g.numel()}")
+            e.data = o.ptr(g, g.dtype, None, f"gradient {i}")
+            e.out = o.ptr(out, out.dtype, None, f"out {i}")
+            e.n, e.dtype, e.out_dtype = g.numel(), _GRAD_TYPES[g.dtype], _GRAD_TYPES[out.dtype]
+        self.index = o.index
+        self.device = torch.device("cuda", o.index)
+        self._seen = seen
+
+    def operands(self, where: str) -> _Operands:
+        self._refresh()
+        o = _Operands(where)
+        o.index = self.index
+        return o
+
+
+def _grad_list(grads, stream) -> GradList:
+    if isinstance(grads, GradList):
+        return grads
+    # a list made for this call alone: its workspace belongs to the call's stream
+    with torch.cuda.stream(stream):
+        return GradList(grads)
+
+
+def moe_grad_sumsq(grads, sumsq, stream=None):
+    """``sumsq`` (1,) fp64 = the sum of the squares of all elements of
+    ``grads`` (a GradList or a sequence of tensors)."""
+    g = _grad_list(grads, stream)
+    o = g.operands("moe_grad_sumsq")
+    out = o.ptr(sumsq, torch.float64, (1,), "sumsq")
+    o.launch(load_library().moe_grad_sumsq, stream, g._entries, g.n, out, g.ws.data_ptr())
+
+
+def moe_grad_scale(grads, sumsq, max_norm: float, norm=None, stream=None):
+    """Scales the gradients by min(1, max_norm / (sqrt(sumsq) + 1e-6)) (1 if
+    that norm is not finite); ``norm`` (1,) fp32 receives sqrt(sumsq)."""
+    g = _grad_list(grads, stream)
+    o = g.operands("moe_grad_scale")
+    src = o.ptr(sumsq, torch.float64, (1,), "sumsq")
+    out = o.ptr(norm, torch.float32, (1,), "norm", True)
+    o.launch(load_library().moe_grad_scale, stream, g._entries, g.n, src, max_norm, out)
+
+
+def moe_clip_grads(grads, max_norm: float, norm=None, stream=None):
+    """Clips the gradients by their global norm (moe_grad_sumsq and
+    moe_grad_scale in one call)."""
+    g = _grad_list(grads, stream)
+    o = g.operands("moe_clip_grads")
+    out = o.ptr(norm, torch.float32, (1,), "norm", True)
+    o.launch(load_library().moe_clip_grads, stream, g._entries, g.n, max_norm, out,
+             g.ws.data_ptr())
 
 
 def moe_selftest_bounded_wait(limit_ns: int, ws, stream=None):

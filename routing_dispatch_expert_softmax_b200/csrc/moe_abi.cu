@@ -1,6 +1,7 @@
 // C ABI of the B200 routed MoE layer: argument checks, workspace carving and
 // the stream-ordered launch sequence.  No allocation, no host synchronisation
 // (except moe_check), no CPU fallback.
+#include <cmath>
 #include <mutex>
 
 #include "moe_kernels.cuh"
@@ -470,6 +471,158 @@ int moe_forward_eplb(const moe_bf16* x, const float* w_g, const float* bias,
   if (r != MOE_OK) return r;
   return cuda_status(
       launch_combine(z, row_of, gw, *s, reinterpret_cast<__nv_bfloat16*>(y), cs));
+}
+
+size_t moe_workspace_size_bwd(const moe_shape* s, int32_t S) {
+  if (!shape_ok(s) || S < 1 || S > kMaxSeqs) return 0;
+  return bwd_layout(*s, S).total;
+}
+
+int moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* token_mask,
+                     const int32_t* seq_offsets, int32_t S, const moe_shape* s,
+                     float balance_coef, float z_coef, float* loss, int32_t* counts,
+                     int32_t* tokens, float* prob_mean, void* ws, void* stream) {
+  if (!shape_ok(s) || S < 1 || S > kMaxSeqs || (!seq_offsets && S != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(balance_coef) || !std::isfinite(z_coef)) return MOE_ERR_INVALID_ARG;
+  if (!ok4(loss) || !ok4(counts) || !ok4(tokens) || (prob_mean && !aligned(prob_mean, 4)) ||
+      !ws || !aligned(ws, 256) || (seq_offsets && !aligned(seq_offsets, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if (s->T > 0 && (!ok4(logits) || !ok4(idx))) return MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  int st = device_check(&sms);
+  if (st != MOE_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (s->T == 0) {
+    cudaError_t e = cudaMemsetAsync(loss, 0, 3 * sizeof(float), cs);
+    const size_t n = (size_t)S * s->E;
+    if (e == cudaSuccess) e = cudaMemsetAsync(counts, 0, n * sizeof(int), cs);
+    if (e == cudaSuccess) e = cudaMemsetAsync(tokens, 0, (S + 2) * sizeof(int), cs);
+    if (e == cudaSuccess && prob_mean) e = cudaMemsetAsync(prob_mean, 0, n * sizeof(float), cs);
+    return cuda_status(e);
+  }
+  return cuda_status(launch_balance_loss(logits, idx, token_mask, seq_offsets, S, *s,
+                                         balance_coef, z_coef, loss, counts, tokens, prob_mean,
+                                         bwd_layout(*s, S), static_cast<char*>(ws), cs));
+}
+
+int moe_gate_bwd(const float* logits, const int32_t* idx, const float* w, const float* dw,
+                 const uint8_t* token_mask, const int32_t* seq_offsets, int32_t S,
+                 const int32_t* counts, const int32_t* tokens, const moe_shape* s,
+                 float balance_coef, float z_coef, const float* dloss, float* dlogits, void* ws,
+                 void* stream) {
+  if (!shape_ok(s) || S < 1 || S > kMaxSeqs || (!seq_offsets && S != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(balance_coef) || !std::isfinite(z_coef)) return MOE_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+  if (s->T == 0) return MOE_OK;
+  if (!ok4(dlogits) || (!dw && !counts)) return MOE_ERR_INVALID_ARG;
+  if (dw && (!ok4(dw) || !ok4(w) || !ok4(idx))) return MOE_ERR_INVALID_ARG;
+  if (counts && (!ok4(counts) || !ok4(tokens) || !ok4(logits) ||
+                 (seq_offsets && !aligned(seq_offsets, 4)) || (dloss && !aligned(dloss, 4))))
+    return MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  int st = device_check(&sms);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_gate_bwd(logits, idx, w, dw, token_mask, seq_offsets, S, counts,
+                                     tokens, *s, balance_coef, z_coef, dloss, dlogits,
+                                     static_cast<int*>(ws), sms,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+int moe_combine_bwd(const moe_bf16* dy, const moe_bf16* z, const int32_t* row_of, const float* w,
+                    const moe_shape* s, float* dw, moe_bf16* dz, void* stream) {
+  if (!shape_ok(s) || (!dw && !dz)) return MOE_ERR_INVALID_ARG;
+  if (s->T == 0) return MOE_OK;
+  if (!ok16(dy) || !ok4(row_of)) return MOE_ERR_INVALID_ARG;
+  if (dw && (!ok4(dw) || !ok16(z))) return MOE_ERR_INVALID_ARG;
+  if (dz && (!ok16(dz) || !ok4(w))) return MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  int st = device_check(&sms);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_combine_bwd(reinterpret_cast<const __nv_bfloat16*>(dy),
+                                        reinterpret_cast<const __nv_bfloat16*>(z), row_of, w, *s,
+                                        dw, reinterpret_cast<__nv_bfloat16*>(dz), sms,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+int moe_router_bwd(const moe_bf16* x, const float* w_g, const float* dlogits, const moe_shape* s,
+                   float* dw_g, float* dbias, moe_bf16* dx, void* ws, void* stream) {
+  if (!shape_ok(s) || (!dw_g && !dbias && !dx)) return MOE_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+  if ((dw_g && !aligned(dw_g, 4)) || (dbias && !aligned(dbias, 4))) return MOE_ERR_INVALID_ARG;
+  if (s->T > 0 && (!ok4(dlogits) || (dw_g && !ok16(x)) || (dx && (!ok16(dx) || !ok4(w_g)))))
+    return MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  int st = device_check(&sms);
+  if (st != MOE_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (s->T == 0) {
+    cudaError_t e = cudaSuccess;
+    if (dw_g) e = cudaMemsetAsync(dw_g, 0, sizeof(float) * s->d * s->E, cs);
+    if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, sizeof(float) * s->E, cs);
+    return cuda_status(e);
+  }
+  return cuda_status(launch_router_bwd(reinterpret_cast<const __nv_bfloat16*>(x), w_g, dlogits,
+                                       *s, dw_g, dbias, reinterpret_cast<__nv_bfloat16*>(dx),
+                                       bwd_layout(*s, 1), static_cast<char*>(ws), cs));
+}
+
+// outs: the entries' outputs are looked at too.
+static bool grads_ok(const moe_grad* g, int32_t n, bool outs) {
+  if (n < 0 || n > 65536 || (n > 0 && !g)) return false;
+  for (int32_t i = 0; i < n; ++i) {
+    if (g[i].n < 0 || g[i].n > (1LL << 40)) return false;
+    if (g[i].dtype != MOE_GRAD_FP32 && g[i].dtype != MOE_GRAD_BF16) return false;
+    if (outs && g[i].out_dtype != MOE_GRAD_FP32 && g[i].out_dtype != g[i].dtype) return false;
+    if (g[i].n == 0) continue;
+    if (!g[i].data || !aligned(g[i].data, g[i].dtype == MOE_GRAD_BF16 ? 2 : 4)) return false;
+    if (!outs) continue;
+    if (!g[i].out || !aligned(g[i].out, g[i].out_dtype == MOE_GRAD_BF16 ? 2 : 4)) return false;
+    if (g[i].out == g[i].data && g[i].out_dtype != g[i].dtype) return false;
+  }
+  return true;
+}
+
+size_t moe_workspace_size_grads(int32_t n) {
+  return n < 0 || n > 65536 ? 0 : grads_ws_bytes(n);
+}
+
+int moe_grad_sumsq(const moe_grad* grads, int32_t n, double* sumsq, void* ws, void* stream) {
+  if (!grads_ok(grads, n, false)) return MOE_ERR_INVALID_ARG;
+  if (!sumsq || !aligned(sumsq, 8) || !ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  int st = device_check(&sms);
+  if (st != MOE_OK) return st;
+  return cuda_status(
+      launch_grad_sumsq(grads, n, sumsq, ws, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_grad_scale(const moe_grad* grads, int32_t n, const double* sumsq, float max_norm,
+                   float* norm_out, void* stream) {
+  if (!grads_ok(grads, n, true) || !(max_norm >= 0.f)) return MOE_ERR_INVALID_ARG;
+  if (!sumsq || !aligned(sumsq, 8) || (norm_out && !aligned(norm_out, 4)))
+    return MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  int st = device_check(&sms);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_grad_scale(grads, n, sumsq, max_norm, norm_out,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+int moe_clip_grads(const moe_grad* grads, int32_t n, float max_norm, float* norm_out, void* ws,
+                   void* stream) {
+  if (!grads_ok(grads, n, true) || !(max_norm >= 0.f)) return MOE_ERR_INVALID_ARG;
+  if ((norm_out && !aligned(norm_out, 4)) || !ws || !aligned(ws, 256))
+    return MOE_ERR_INVALID_ARG;
+  int sms = 0;
+  int st = device_check(&sms);
+  if (st != MOE_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  double* sumsq = grads_ws_sumsq(ws);
+  cudaError_t e = launch_grad_sumsq(grads, n, sumsq, ws, cs);
+  if (e == cudaSuccess) e = launch_grad_scale(grads, n, sumsq, max_norm, norm_out, cs);
+  return cuda_status(e);
 }
 
 int moe_selftest_bounded_wait(long long limit_ns, void* ws, void* stream) {

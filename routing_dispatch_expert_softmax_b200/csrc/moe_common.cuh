@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/moe.h"
 
 namespace moe {
@@ -58,8 +60,9 @@ inline int router_tc_parts(const moe_shape& s) {
 
 // Workspace header (the 64 bytes the caller zeroes once): ws[0] = first error
 // code, ws[1] = detail (kernel id), ws[2] = the fused routing kernel's block
-// ticket (back to 0 at the end of every call).
-enum : int { kErrSlot = 0, kErrDetail = 1, kRouteTicket = 2 };
+// ticket, ws[3] = the balance loss' and ws[4] = the gradient norm's (each back
+// to 0 at the end of every call).
+enum : int { kErrSlot = 0, kErrDetail = 1, kRouteTicket = 2, kBalanceTicket = 3, kGradTicket = 4 };
 
 // Every bounded wait gives up after this many nanoseconds of %globaltimer.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
@@ -184,6 +187,48 @@ inline WsLayout ws_layout(const moe_shape& s, int num_sms, int E_tab = -1) {
   L.hq = take((size_t)L.Ppad * f);
   L.hs = take(sizeof(float) * (size_t)L.Ppad);
   L.total = o;
+  return L;
+}
+
+// Workspace of the gate's training calls (moe_workspace_size_bwd).  The balance
+// loss and the router's backward each use the region after the header as their
+// own scratch; nothing in it outlives a call.
+constexpr int kMaxSeqs = 65535;
+struct BwdLayout {
+  // balance loss: blocks of `chunk` tokens, one partial per (block, sequence)
+  // pair that meets (at most blocks + S of them)
+  int chunk;
+  size_t prob, count, z, n, term, zterm;
+  // router backward: the tokens in dw_parts parts, a partial dW each
+  int dw_parts;
+  size_t dw_part;
+  size_t total;
+};
+
+inline BwdLayout bwd_layout(const moe_shape& s, int S) {
+  BwdLayout L{};
+  const long long T = s.T, d = s.d, E = s.E;
+  size_t o = 256;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 256);
+    return at;
+  };
+  // 32 tokens a block (4 for each warp) until 592 blocks, 4 on each SM, are full
+  L.chunk = (int)(T <= 32 * 592 ? 32 : (T + 591) / 592);
+  const size_t slots = (size_t)((T + L.chunk - 1) / L.chunk) + S;
+  L.prob = take(sizeof(float) * slots * E);
+  L.count = take(sizeof(int) * slots * E);
+  L.z = take(sizeof(float) * slots);
+  L.n = take(sizeof(int) * slots);
+  L.term = take(sizeof(double) * (size_t)S * ((E + 31) / 32));
+  L.zterm = take(sizeof(double) * S);
+  const size_t balance = o;
+  o = 256;
+  const long long tiles = (d / 64) * ((E + 63) / 64);
+  L.dw_parts = (int)std::max(1LL, std::min((T + 255) / 256, 592 / tiles));
+  L.dw_part = take(sizeof(float) * (size_t)L.dw_parts * d * E);
+  L.total = std::max(balance, o);
   return L;
 }
 

@@ -92,4 +92,33 @@ cudaError_t launch_eplb_remap(const int* idx, int T, int k, int E, const int* re
                               const int* rep_phys, int P, int* idx_phys, int* err,
                               cudaStream_t st);
 
+// Training the gate (moe_gate_train.cu): the balance loss over S sequences
+// (off == nullptr: one, all tokens), the router logits' gradient, and the
+// combine's backward.
+cudaError_t launch_balance_loss(const float* logits, const int* idx, const uint8_t* mask,
+                                const int* off, int S, const moe_shape& s, float balance_coef,
+                                float z_coef, float* loss, int* counts, int* tokens,
+                                float* prob_mean, const BwdLayout& L, char* ws, cudaStream_t st);
+cudaError_t launch_gate_bwd(const float* logits, const int* idx, const float* w, const float* dw,
+                            const uint8_t* mask, const int* off, int S, const int* counts,
+                            const int* tokens, const moe_shape& s, float balance_coef,
+                            float z_coef, const float* dloss, float* dlogits, int* err, int sms,
+                            cudaStream_t st);
+cudaError_t launch_combine_bwd(const __nv_bfloat16* dy, const __nv_bfloat16* z, const int* row_of,
+                               const float* w, const moe_shape& s, float* dw, __nv_bfloat16* dz,
+                               int sms, cudaStream_t st);
+
+// The router's backward (moe_router_bwd.cu); any of dw, db, dx may be null.
+cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const float* dl,
+                              const moe_shape& s, float* dw, float* db, __nv_bfloat16* dx,
+                              const BwdLayout& L, char* ws, cudaStream_t st);
+
+// Global gradient norm and clipping (moe_grads.cu); the workspace holds the
+// header, a sum for moe_clip_grads, and the blocks' partial sums.
+size_t grads_ws_bytes(int n);
+double* grads_ws_sumsq(void* ws);
+cudaError_t launch_grad_sumsq(const moe_grad* g, int n, double* sumsq, void* ws, cudaStream_t st);
+cudaError_t launch_grad_scale(const moe_grad* g, int n, const double* sumsq, float max_norm,
+                              float* norm, cudaStream_t st);
+
 }  // namespace moe
