@@ -565,7 +565,7 @@ int moe_router_bwd(const moe_bf16* x, const float* w_g, const float* dlogits, co
   }
   return cuda_status(launch_router_bwd(reinterpret_cast<const __nv_bfloat16*>(x), w_g, dlogits,
                                        *s, dw_g, dbias, reinterpret_cast<__nv_bfloat16*>(dx),
-                                       bwd_layout(*s, 1), static_cast<char*>(ws), cs));
+                                       bwd_layout(*s, 1), static_cast<char*>(ws), sms, cs));
 }
 
 // outs: the entries' outputs are looked at too.

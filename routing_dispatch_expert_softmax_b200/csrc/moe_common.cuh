@@ -199,11 +199,37 @@ struct BwdLayout {
   // pair that meets (at most blocks + S of them)
   int chunk;
   size_t prob, count, z, n, term, zterm;
-  // router backward: the tokens in dw_parts parts, a partial dW each
-  int dw_parts;
-  size_t dw_part;
+  // router backward: bf16 planes of dlogits [3][T][cp] and w_g [2][d][cp]
+  // (cp = E rounded up to 64), column sums of every plane_rows tokens, and
+  // partial weight gradients of the token ranges
+  int cp, plane_rows;
+  size_t dl_planes, w_planes, db_part, dw_part;
   size_t total;
 };
+
+// The router's backward cuts the tokens of dW into ranges: more of them fill the
+// SMs, but each writes a partial dW that is read again.  In units of one
+// 64-token block of a 128 x 256 tile (0.8 us): all tiles' blocks and dx's 64-
+// expert blocks over 148 SMs, but no less than the blocks of the longest SM's
+// items (with an epilogue of 1.5 each), plus 0.06 for each partial tile's way to L2
+// and back.  The number of ranges with the least sum is taken; what is returned is
+// the 64-token blocks of one range.
+inline int router_range_blocks(const moe_shape& s, bool dx) {
+  const long long tiles = (long long)((s.d + 255) / 256) * ((s.E + 127) / 128);
+  const long long blocks = ((long long)s.T + 63) / 64;
+  const double dx_work =
+      dx ? (double)((s.T + 127) / 128) * ((s.d + 255) / 256) * ((s.E + 63) / 64) : 0.0;
+  long long best = std::max(1LL, blocks);
+  double least = 0.0;
+  for (long long r = 1; r <= std::min(blocks, 148LL); ++r) {
+    const long long per = (blocks + r - 1) / r, n = (blocks + per - 1) / per;
+    const double waves = (double)((tiles * n + 147) / 148);
+    const double cost = std::max(waves * (per + 1.5), (tiles * blocks + dx_work) / 148) +
+                        (n > 1 ? 0.06 * tiles * n : 0.0);
+    if (r == 1 || cost < least) best = per, least = cost;
+  }
+  return (int)best;
+}
 
 inline BwdLayout bwd_layout(const moe_shape& s, int S) {
   BwdLayout L{};
@@ -225,9 +251,14 @@ inline BwdLayout bwd_layout(const moe_shape& s, int S) {
   L.zterm = take(sizeof(double) * S);
   const size_t balance = o;
   o = 256;
-  const long long tiles = (d / 64) * ((E + 63) / 64);
-  L.dw_parts = (int)std::max(1LL, std::min((T + 255) / 256, 592 / tiles));
-  L.dw_part = take(sizeof(float) * (size_t)L.dw_parts * d * E);
+  L.cp = (int)align_up(E, 64);
+  L.plane_rows = (int)std::max(16LL, (T + 591) / 592);
+  L.dl_planes = take(2 * 3 * (size_t)T * L.cp);
+  L.w_planes = take(2 * 2 * (size_t)d * L.cp);
+  L.db_part = take(sizeof(float) * (size_t)((T + L.plane_rows - 1) / L.plane_rows) * E);
+  const long long per = std::min(router_range_blocks(s, false), router_range_blocks(s, true));
+  const long long ranges = ((T + 63) / 64 + per - 1) / per;
+  L.dw_part = take(ranges > 1 ? sizeof(float) * (size_t)ranges * d * E : 0);
   L.total = std::max(balance, o);
   return L;
 }
