@@ -199,34 +199,56 @@ struct BwdLayout {
   // pair that meets (at most blocks + S of them)
   int chunk;
   size_t prob, count, z, n, term, zterm;
-  // router backward: bf16 planes of dlogits [3][T][cp] and w_g [2][d][cp]
-  // (cp = E rounded up to 64), column sums of every plane_rows tokens, and
+  // router backward: bf16 planes of dlogits (router_planes), fp16 dlogits [T][cp]
+  // and w_g [d][cp] (cp = E rounded up to 64) with the factors that undo their rows' scaling, column sums of every plane_rows tokens, and
   // partial weight gradients of the token ranges
   int cp, plane_rows;
-  size_t dl_planes, w_planes, db_part, dw_part;
+  size_t dl_planes, dl_half, w_half, dl_back, w_back, db_part, dw_part;
   size_t total;
 };
 
-// The router's backward cuts the tokens of dW into ranges: more of them fill the
-// SMs, but each writes a partial dW that is read again.  In units of one
-// 64-token block of a 128 x 256 tile (0.8 us): all tiles' blocks and dx's 64-
-// expert blocks over 148 SMs, but no less than the blocks of the longest SM's
-// items (with an epilogue of 1.5 each), plus 0.06 for each partial tile's way to L2
-// and back.  The number of ranges with the least sum is taken; what is returned is
-// the 64-token blocks of one range.
+// How the router's backward lays dL's three bf16 planes out for dW's 128-row MMA
+// operand: above 64 experts a plane of its own each (three MMAs for each K step);
+// up to 64, side by side in rows of (hi | mid | lo | 0) x 64 (two MMAs); up to
+// 32, of x 32 (one).  Side by side, a plane's rows of the product are apart, so a
+// tile is `parts` partial weight gradients.
+struct RouterPlanes {
+  int sets, parts, width;  // MMAs for each K step; partials; columns of one plane
+};
+inline RouterPlanes router_planes(int E) {
+  if (E <= 32) return {1, 3, 32};
+  if (E <= 64) return {2, 2, 64};
+  return {3, 1, (int)((E + 63) / 64 * 64)};
+}
+
+// Times in us that the router's backward plans with (1.85 GHz, 6.5 TB/s over 148
+// SMs): a 64-token block of a 128 x 256 tile of dW, MMAs or the 32 KB of x; a 128 x
+// 256 tile of dx, MMAs or about its 64 KB of output.
+inline double router_dw_block_us(int E) { return std::max(0.28 * router_planes(E).sets, 0.74); }
+inline double router_dx_tile_us(int E) { return std::max(0.28 * ((E + 63) / 64), 1.2); }
+
+// The tokens of dW are cut into ranges: more of them fill the SMs, but each
+// writes partials that are read again.  The time of `r` ranges: all work over
+// 148 SMs, but no less than the longest SM's dW items (each with 1.2 us of
+// start and end), plus each partial's way to L2 and back.  The r with the least
+// time is taken; what is returned is the 64-token blocks of one range.
 inline int router_range_blocks(const moe_shape& s, bool dx) {
-  const long long tiles = (long long)((s.d + 255) / 256) * ((s.E + 127) / 128);
+  const RouterPlanes pl = router_planes(s.E);
+  const double kb = router_dw_block_us(s.E);
+  const long long cols = (s.d + 255) / 256;
+  const long long tiles = cols * (pl.sets == 3 ? (s.E + 127) / 128 : 1);
   const long long blocks = ((long long)s.T + 63) / 64;
-  const double dx_work =
-      dx ? (double)((s.T + 127) / 128) * ((s.d + 255) / 256) * ((s.E + 63) / 64) : 0.0;
+  const double dx_us = dx ? (double)((s.T + 127) / 128) * cols * router_dx_tile_us(s.E) : 0.0;
+  const double partial_us = 8.0 * pl.parts * s.d * s.E / 5e6;  // written and read at 5 TB/s
   long long best = std::max(1LL, blocks);
   double least = 0.0;
   for (long long r = 1; r <= std::min(blocks, 148LL); ++r) {
     const long long per = (blocks + r - 1) / r, n = (blocks + per - 1) / per;
     const double waves = (double)((tiles * n + 147) / 148);
-    const double cost = std::max(waves * (per + 1.5), (tiles * blocks + dx_work) / 148) +
-                        (n > 1 ? 0.06 * tiles * n : 0.0);
-    if (r == 1 || cost < least) best = per, least = cost;
+    const double us = std::max(waves * (per * kb + 1.2),
+                               (tiles * (blocks * kb + n * 1.2) + dx_us) / 148) +
+                      n * partial_us;
+    if (r == 1 || us < least) best = per, least = us;
   }
   return (int)best;
 }
@@ -252,13 +274,17 @@ inline BwdLayout bwd_layout(const moe_shape& s, int S) {
   const size_t balance = o;
   o = 256;
   L.cp = (int)align_up(E, 64);
-  L.plane_rows = (int)std::max(16LL, (T + 591) / 592);
-  L.dl_planes = take(2 * 3 * (size_t)T * L.cp);
-  L.w_planes = take(2 * 2 * (size_t)d * L.cp);
+  L.plane_rows = (int)std::max(32LL, (T + 591) / 592);
+  const RouterPlanes pl = router_planes(s.E);
+  L.dl_planes = take(2 * (size_t)T * pl.width * (pl.sets == 3 ? 3 : 4));
+  L.dl_half = take(2 * (size_t)T * L.cp);
+  L.w_half = take(2 * (size_t)d * L.cp);
+  L.dl_back = take(2 * (size_t)T);
+  L.w_back = take(2 * (size_t)d);
   L.db_part = take(sizeof(float) * (size_t)((T + L.plane_rows - 1) / L.plane_rows) * E);
   const long long per = std::min(router_range_blocks(s, false), router_range_blocks(s, true));
   const long long ranges = ((T + 63) / 64 + per - 1) / per;
-  L.dw_part = take(ranges > 1 ? sizeof(float) * (size_t)ranges * d * E : 0);
+  L.dw_part = take(ranges * pl.parts > 1 ? sizeof(float) * (size_t)ranges * pl.parts * d * E : 0);
   L.total = std::max(balance, o);
   return L;
 }

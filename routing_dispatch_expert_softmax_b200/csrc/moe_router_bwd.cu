@@ -1,17 +1,22 @@
 // Backward of the router product L = x W_g + b:
 //   dW[i,e] = sum_t x[t,i] dL[t,e],  db[e] = sum_t dL[t,e],
 //   dx[t,i] = sum_e dL[t,e] W[i,e]
-// on the sm_100a tensor cores.  dL and W are fp32; the tensor cores take
-// bf16.  A first kernel splits them into bf16 planes, hi = bf16(v),
-// mid = bf16(v - hi), lo = bf16(v - hi - mid), so hi + mid + lo = v to more
-// than 24 bits:
-//   dW = x (hi + mid + lo): x is bf16, so the three products are exact and the
-//        result is an fp32 product's;
-//   dx = dL_hi W_hi + dL_mid W_hi + dL_hi W_mid, what is left out is below
-//        3 * 2^-18 of each product (dx itself is rounded to 2^-8).
+// on the sm_100a tensor cores.  dL and W are fp32; the tensor cores take 16-bit
+// operands.  A first kernel prepares them:
+//   dW: dL splits into three bf16 planes, hi = bf16(v), mid = bf16(v - hi),
+//       lo = bf16(v - hi - mid), hi + mid + lo = v to more than 24 bits.  x is
+//       bf16, so the three products are exact and dW is as good as an fp32
+//       product's;
+//   dx: dx is rounded to bf16 (2^-8), so dL and W are rounded to fp16, which
+//       keeps 2^-11 of each value: a third of the MMAs that planes of both
+//       would take.  Each row is first scaled by a power of two that brings
+//       its largest value to [2^14, 2^15), so that no value overflows and only
+//       those below 2^-28 of the row's largest lose bits; the epilogue scales back.
 // One persistent kernel then runs the tiles of both products.  The tokens are
 // the long axis of dW, so its tiles split over token ranges; a last kernel
 // adds the ranges' partial tiles in order.
+#include <cuda_fp16.h>
+
 #include "moe_kernels.cuh"
 
 namespace moe {
@@ -35,81 +40,136 @@ __device__ __forceinline__ Split3 split3(float v) {
   return s;
 }
 
-// planes[p][row][0 .. cp) of the [rows, cols] fp32 matrix a, cp = cols rounded
-// up to 64 with zeros.  Each thread takes 8 columns of every (256 / (cp / 8))-th
-// row of the block's; with sums != nullptr the block also stores its rows'
-// column sums as sums[block][cols].
+// The power of two that brings |top| to [2^14, 2^15), and its inverse (1 for
+// 0, inf and NaN; at most 2^126, for rows below 2^-112).
+__device__ __forceinline__ void half_scale(float top, float& scale, float& back) {
+  const int e = (__float_as_int(top) >> 23) & 0xff;  // top >= 0; biased exponent
+  const int f = e == 255 || top == 0.f ? 0 : min(126, 127 + 14 - e);
+  scale = __int_as_float((f + 127) << 23);
+  back = __int_as_float((127 - f) << 23);
+}
+
+// One [rows, cols] fp32 matrix a; every output is optional:
+//   planes                its bf16 planes: plane p of row r at r * row + p * plane,
+//                         `width` columns (zeros from cols on); with zero_plane a
+//                         fourth of zeros
+//   half [rows][cp], back [rows]  its rows scaled and rounded to fp16, cp = cols
+//                         rounded up to 64 with zeros, and the factors that undo
+//                         the scaling
+//   sums [block][cols]    column sums of each block's rows
 struct PlanesArgs {
   const float* a;
-  __nv_bfloat16* planes;  // nullptr: only the sums
+  __nv_bfloat16* planes;
+  __half* half;
+  __nv_bfloat16* back;
   float* sums;
-  long long rows;
-  int cols, cp, nplanes, rows_per_block, blocks, vec;
+  long long rows, row, plane;
+  int cols, cp, width, zero_plane, rows_per_block, blocks, vec;
 };
 
+// G lanes take a row, 8 neighbouring columns of every 8 G-th.
+template <int G, int NO>
 __device__ void planes_block(const PlanesArgs& p, int block, float* red) {
-  const int oct = p.cp / 8, par = 256 / oct;
-  const int o = threadIdx.x % oct, r0 = threadIdx.x / oct;
+  constexpr int kPar = 256 / G;
+  const int l = threadIdx.x % G, g = threadIdx.x / G;
   const long long first = (long long)block * p.rows_per_block;
   const long long last = min(p.rows, first + p.rows_per_block);
-  const int c0 = 8 * o;
-  float sum[8];
+  float sum[NO][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-  if (r0 < par) {
-    for (long long r = first + r0; r < last; r += par) {
+  for (int n = 0; n < NO; ++n)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[n][i] = 0.f;
+  for (long long r0 = first; r0 < last; r0 += kPar) {
+    const long long r = r0 + g;
+    float v[NO][8], top = 0.f;
+#pragma unroll
+    for (int n = 0; n < NO; ++n) {
+      const int c0 = 8 * (l + n * G);
       const float* src = p.a + r * p.cols + c0;
-      float v[8];
-      if (p.vec && c0 + 8 <= p.cols) {
+      if (r < last && p.vec && c0 + 8 <= p.cols) {
         const float4 x = __ldg(reinterpret_cast<const float4*>(src));
         const float4 y = __ldg(reinterpret_cast<const float4*>(src) + 1);
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-        v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+        v[n][0] = x.x, v[n][1] = x.y, v[n][2] = x.z, v[n][3] = x.w;
+        v[n][4] = y.x, v[n][5] = y.y, v[n][6] = y.z, v[n][7] = y.w;
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c0 + i < p.cols ? __ldg(src + i) : 0.f;
+        for (int i = 0; i < 8; ++i)
+          v[n][i] = r < last && c0 + i < p.cols ? __ldg(src + i) : 0.f;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += v[i];
-      if (p.planes) {
+      for (int i = 0; i < 8; ++i) {
+        sum[n][i] += v[n][i];
+        top = fmaxf(top, fabsf(v[n][i]));
+      }
+    }
+    float scale = 1.f, back = 1.f;
+    if (p.half) {
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      half_scale(top, scale, back);
+      if (l == 0 && r < last) p.back[r] = __float2bfloat16_rn(back);
+    }
+#pragma unroll
+    for (int n = 0; n < NO; ++n) {
+      const int c0 = 8 * (l + n * G);
+      if (r >= last || c0 >= p.cp) continue;
+      if (p.planes && c0 < p.width) {
         uint32_t w[3][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const Split3 a = split3(v[2 * i]), b = split3(v[2 * i + 1]);
+          const Split3 a = split3(v[n][2 * i]), b = split3(v[n][2 * i + 1]);
           const __nv_bfloat162 h = __halves2bfloat162(a.hi, b.hi);
           const __nv_bfloat162 m = __halves2bfloat162(a.mid, b.mid);
-          const __nv_bfloat162 l = __halves2bfloat162(a.lo, b.lo);
+          const __nv_bfloat162 q = __halves2bfloat162(a.lo, b.lo);
           w[0][i] = *reinterpret_cast<const uint32_t*>(&h);
           w[1][i] = *reinterpret_cast<const uint32_t*>(&m);
-          w[2][i] = *reinterpret_cast<const uint32_t*>(&l);
+          w[2][i] = *reinterpret_cast<const uint32_t*>(&q);
         }
-        for (int q = 0; q < p.nplanes; ++q)
-          *reinterpret_cast<uint4*>(p.planes + ((size_t)q * p.rows + r) * p.cp + c0) =
-              q == 0   ? make_uint4(w[0][0], w[0][1], w[0][2], w[0][3])
-              : q == 1 ? make_uint4(w[1][0], w[1][1], w[1][2], w[1][3])
-                       : make_uint4(w[2][0], w[2][1], w[2][2], w[2][3]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          *reinterpret_cast<uint4*>(p.planes + r * p.row + q * p.plane + c0) =
+              make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+        if (p.zero_plane)
+          *reinterpret_cast<uint4*>(p.planes + r * p.row + 3 * p.plane + c0) =
+              make_uint4(0, 0, 0, 0);
+      }
+      if (p.half) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 h = __floats2half2_rn(v[n][2 * i] * scale, v[n][2 * i + 1] * scale);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(p.half + (size_t)r * p.cp + c0) =
+            make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   }
   if (!p.sums) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (r0 < par) red[(size_t)r0 * p.cp + c0 + i] = sum[i];
+  for (int n = 0; n < NO; ++n)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = 8 * (l + n * G) + i;
+      if (c < p.cp) red[g * p.cp + c] = sum[n][i];
+    }
   __syncthreads();
   for (int c = threadIdx.x; c < p.cols; c += 256) {
     float s = 0.f;
-    for (int r = 0; r < par; ++r) s += red[(size_t)r * p.cp + c];
+#pragma unroll 8
+    for (int r = 0; r < kPar; ++r) s += red[r * p.cp + c];
     p.sums[(size_t)block * p.cols + c] = s;
   }
 }
 
-// Blocks [0, a.blocks) split dL, the others W.
+// Blocks [0, dl.blocks) prepare dL, the others W.
+template <int G, int NO>
 __global__ void __launch_bounds__(256) k_router_planes(const PlanesArgs dl, const PlanesArgs w) {
-  __shared__ float red[256 * 8];
+  extern __shared__ float sm[];  // [256 / G][cp]
   pdl_trigger();
   pdl_wait();
-  if ((int)blockIdx.x < dl.blocks) planes_block(dl, blockIdx.x, red);
-  else planes_block(w, blockIdx.x - dl.blocks, red);
+  if ((int)blockIdx.x < dl.blocks) planes_block<G, NO>(dl, blockIdx.x, sm);
+  else planes_block<G, NO>(w, blockIdx.x - dl.blocks, sm);
 }
 
 // ============================================================== products
@@ -117,13 +177,15 @@ __global__ void __launch_bounds__(256) k_router_planes(const PlanesArgs dl, cons
 //   dW: rows = 128 experts, columns = 256 of d, K = the tokens of one range;
 //       A = dL planes and B = x, both with the non-K index contiguous
 //       (MN-major): tiles of 64 tokens x 64 columns, 128 bytes a row;
-//   dx: rows = 128 tokens, columns = 256 of d, K = experts; A = dL planes and
-//       B = W planes, both K-major.
+//   dx: rows = 128 tokens, columns = 256 of d, K = experts; A = dL and B = W in
+//       fp16, both K-major.
 // dW takes the experts as rows so that a row of 256 columns of x serves the
 // three planes, and a lane's accumulator row is one expert: the 32 lanes of a
 // warp then store 32 neighbouring experts of dW[i, :].
 // Shared memory: a ring of 16 KB A tiles and one of 32 KB B tiles (128-byte
-// swizzle).  For each 64 of K, dW takes 3 A and 1 B tiles, dx 2 and 2.
+// swizzle).  For each 64 of K, dW takes `sets` A (RouterPlanes) and 1 B tiles, dx one of each; with
+// up to 256 experts a block keeps the W tiles of its 256 columns in the B ring
+// while it goes down the tokens, so that a dx item loads 64 KB at most.
 //
 // The tensor cores cut, not round, when they add to an fp32 accumulator, so a
 // sum is short by about 2^-25 of itself for every MMA in a row (measured: dW
@@ -139,11 +201,14 @@ struct RouterGemmArgs {
   int T, d, E;
   int dw_items, dx_items;
   int ne, nd;            // expert and column tiles of dW
+  int sets, parts;       // RouterPlanes
   int kblocks, kper;     // 64-token blocks in all, and of one range
-  int xt;                // column tiles of dx
+  int mt;                // token tiles of dx
   int kx;                // 64-expert blocks of dx
   int light_dx;          // dx items of the blocks that have one dW item less
-  float* dw;             // [ranges][d][E]
+  const __nv_bfloat16* dl_back;  // [T], [d]: factors that undo the fp16 scaling
+  const __nv_bfloat16* w_back;
+  float* dw;             // [ranges][parts][d][E]
   int* err;
 };
 
@@ -161,9 +226,9 @@ __device__ __forceinline__ void dx_run(const RouterGemmArgs& a, int c, int g, in
 }
 
 constexpr int kChunk = 2;
-constexpr int kRA = 6, kRB = 3;
+constexpr int kRA = 4, kRB = 4;
 constexpr int kATile = 128 * 64 * 2, kBTile = 256 * 64 * 2;
-constexpr int kStageOut = 32 * 128;  // per epilogue warp: 32 rows x 64 bf16 of dx
+constexpr int kStageOut = 2 * 32 * 64;  // per epilogue warp: two times 32 rows x 32 bf16 of dx
 constexpr int kRouterSmem = kRA * kATile + kRB * kBTile + 8 * kStageOut + 1024 + 256;
 constexpr int kRouterThreads = 320;  // TMA, MMA and eight epilogue warps
 
@@ -267,6 +332,7 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------ TMA producer
+      const uint64_t policy = policy_evict_normal();
       Ring a, b;
       int a_fills[kRA], b_fills[kRB];
 #pragma unroll
@@ -294,27 +360,31 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
           if (!(ok = dst != nullptr)) break;
           tma_load_3d(dst, &tm_x, &b_full[b.slot], 0, kb * 64, dt * 4);
           b.next(kRB);
-          for (int p = 2; p >= 0; --p) {
+          for (int p = args.sets - 1; p >= 0; --p) {
             dst = take_a();
             if (!(ok = dst != nullptr)) break;
-            tma_load_4d(dst, &tm_dl_mn, &a_full[a.slot], 0, kb * 64, et * 2, p);
+            const bool apart = args.sets == 3;  // each plane for itself
+            tma_load_4d(dst, &tm_dl_mn, &a_full[a.slot], 0, kb * 64, apart ? et * 2 : p * 2,
+                        apart ? p : 0);
             a.next(kRA);
           }
         }
       }
+      int nt = dx0 / args.mt, mt = dx0 - nt * args.mt;
       for (int w = dx0; w < dx1 && ok; ++w) {
-        const int nt = w % args.xt, mt = w / args.xt;
-        for (int kb = 0; kb < args.kx && ok; ++kb)
-          for (int p = 0; p < 2; ++p) {
-            uint8_t* dst = take_a();
-            if (!(ok = dst != nullptr)) break;
-            tma_load_3d(dst, &tm_dl_k, &a_full[a.slot], kb * 64, mt * 128, p);
-            a.next(kRA);
-            dst = take_b();
-            if (!(ok = dst != nullptr)) break;
-            tma_load_3d(dst, &tm_w, &b_full[b.slot], kb * 64, nt * 256, p);
-            b.next(kRB);
-          }
+        const bool load_b = args.kx > kRB || w == dx0 || mt == 0;
+        for (int kb = 0; kb < args.kx && ok; ++kb) {
+          uint8_t* dst = take_a();
+          if (!(ok = dst != nullptr)) break;
+          tma_load_2d(dst, &tm_dl_k, &a_full[a.slot], kb * 64, mt * 128, policy);
+          a.next(kRA);
+          if (!load_b) continue;
+          dst = take_b();
+          if (!(ok = dst != nullptr)) break;
+          tma_load_2d(dst, &tm_w, &b_full[b.slot], kb * 64, nt * 256, policy);
+          b.next(kRB);
+        }
+        if (++mt == args.mt) mt = 0, ++nt;
       }
       if (*abort_flag) {
         // Let every copy already issued land before the CTA leaves.
@@ -332,29 +402,21 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
   } else if (warp == 1) {
     if (lane == 0) {
       // ------------------------------------------------ MMA issuer
-      constexpr uint32_t kIdescK = idesc_bf16_f32(128, 256);
-      constexpr uint32_t kIdescMn = kIdescK | 1u << 15 | 1u << 16;  // A and B MN-major
+      // One thread's scalar work for a tile has to stay below its MMAs' 512
+      // cycles: descriptors are a base plus a slot's offset, no divisions, and W's
+      // tiles are waited for once (with all of that left out of this, a dx item
+      // took 4,400 cycles, twice its MMAs).
+      // bf16 A and B, both MN-major
+      constexpr uint32_t kIdescMn = idesc_bf16_f32(128, 256) | 1u << 15 | 1u << 16;
+      // fp16 A and B (format code 0 in bits [7, 10) and [10, 13)), K-major
+      constexpr uint32_t kIdescK = idesc_bf16_f32(128, 256) & ~(1u << 7 | 1u << 10);
+      constexpr uint64_t kA = kATile >> 4, kB = kBTile >> 4;  // descriptor units of a slot
+      const uint64_t a_mn = sw128_mnmajor_desc(smem_u32(sa)), b_mn = sw128_mnmajor_desc(smem_u32(sb));
+      const uint64_t a_k = sw128_kmajor_desc(smem_u32(sa)), b_k = sw128_kmajor_desc(smem_u32(sb));
       Ring a, b;
       bool ok = true;
-      // four K = 16 steps of one pair of tiles
-      auto mma_mn = [&](uint32_t d, int sa_slot, int sb_slot, uint32_t acc) {
-        const uint32_t aa = smem_u32(sa + sa_slot * kATile), bb = smem_u32(sb + sb_slot * kBTile);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_bf16_ss(d, sw128_mnmajor_desc(aa + kk * 2048), sw128_mnmajor_desc(bb + kk * 2048),
-                       kIdescMn, kk ? 1u : acc);
-      };
-      auto mma_k = [&](uint32_t d, int sa_slot, int sb_slot, uint32_t acc) {
-        const uint32_t aa = smem_u32(sa + sa_slot * kATile), bb = smem_u32(sb + sb_slot * kBTile);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_bf16_ss(d, sw128_kmajor_desc(aa + kk * 32), sw128_kmajor_desc(bb + kk * 32),
-                       kIdescK, kk ? 1u : acc);
-      };
       auto wait = [&](uint64_t* bar, uint32_t phase) {
-        const bool got = mbar_wait_bounded(bar, phase, abort_flag);
-        tc_fence_after();
-        return got;
+        return mbar_try_wait(bar, phase) || mbar_wait_bounded(bar, phase, abort_flag);
       };
       int it = 0;  // accumulators filled so far
       for (int w = blockIdx.x; w < args.dw_items && ok; w += gridDim.x) {
@@ -363,12 +425,20 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
         for (int c0 = range * args.kper; c0 < kb1 && ok; c0 += kChunk, ++it) {
           const int ab = it & 1;
           if (!(ok = wait(&tempty[ab], ((it >> 1) & 1) ^ 1u))) break;
+          tc_fence_after();
           const uint32_t d = tmem_base + (uint32_t)(ab * 256);
+          uint32_t acc = 0;
           for (int kb = c0; kb < min(kb1, c0 + kChunk) && ok; ++kb) {
             if (!(ok = wait(&b_full[b.slot], b.phase))) break;
-            for (int p = 0; p < 3; ++p) {
+            const uint64_t db = b_mn + b.slot * kB;
+            for (int p = 0; p < args.sets; ++p) {
               if (!(ok = wait(&a_full[a.slot], a.phase))) break;
-              mma_mn(d, a.slot, b.slot, kb != c0 || p != 0);
+              const uint64_t da = a_mn + a.slot * kA;
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {  // 16 K rows of 128 bytes each
+                umma_bf16_ss(d, da + kk * (2048 >> 4), db + kk * (2048 >> 4), kIdescMn, acc);
+                acc = 1;
+              }
               umma_commit(&a_empty[a.slot]);
               a.next(kRA);
             }
@@ -378,30 +448,32 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
           if (ok) umma_commit(&tfull[ab]);
         }
       }
+      // W's tiles stay until the last item of a block of columns (or, with too
+      // many experts for the ring, are new for each item).
+      const bool keep = args.kx <= kRB;
+      Ring b0;
+      int mt = dx0 < dx1 ? dx0 % args.mt : 0;
       for (int w = dx0; w < dx1 && ok; ++w, ++it) {
         const int ab = it & 1;
-        if (!wait(&tempty[ab], ((it >> 1) & 1) ^ 1u)) break;
+        if (!(ok = wait(&tempty[ab], ((it >> 1) & 1) ^ 1u))) break;
+        tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(ab * 256);
-        for (int kb = 0; kb < args.kx && ok; ++kb) {
-          const Ring ahi = a;
+        const bool new_b = !keep || w == dx0 || mt == 0;
+        if (++mt == args.mt) mt = 0;
+        const bool free_b = !keep || w + 1 == dx1 || mt == 0;
+        if (new_b) b0 = b;
+        b = b0;
+        for (int kb = 0; kb < args.kx; ++kb) {
+          if (new_b && !(ok = wait(&b_full[b.slot], b.phase))) break;
+          if (!(ok = wait(&a_full[a.slot], a.phase))) break;
+          const uint64_t da = a_k + a.slot * kA, db = b_k + b.slot * kB;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 16 K columns of 2 bytes each
+            umma_bf16_ss(d, da + kk * (32 >> 4), db + kk * (32 >> 4), kIdescK, (kb | kk) ? 1u : 0u);
+          umma_commit(&a_empty[a.slot]);
           a.next(kRA);
-          const Ring amid = a;
-          a.next(kRA);
-          const Ring bhi = b;
+          if (free_b) umma_commit(&b_empty[b.slot]);
           b.next(kRB);
-          const Ring bmid = b;
-          b.next(kRB);
-          if (!(ok = wait(&a_full[ahi.slot], ahi.phase) && wait(&b_full[bhi.slot], bhi.phase)))
-            break;
-          mma_k(d, ahi.slot, bhi.slot, kb != 0);
-          if (!(ok = wait(&a_full[amid.slot], amid.phase))) break;
-          mma_k(d, amid.slot, bhi.slot, 1);
-          umma_commit(&a_empty[amid.slot]);
-          umma_commit(&b_empty[bhi.slot]);
-          if (!(ok = wait(&b_full[bmid.slot], bmid.phase))) break;
-          mma_k(d, ahi.slot, bmid.slot, 1);
-          umma_commit(&a_empty[ahi.slot]);
-          umma_commit(&b_empty[bmid.slot]);
         }
         if (ok) umma_commit(&tfull[ab]);
       }
@@ -447,9 +519,13 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
         }
         release();
       }
-      const int e = et * 128 + q * 32 + lane, col = dt * 256 + half * 128;
-      float* out = args.dw + ((size_t)range * args.d + col) * args.E + e;
-      if (ok && e < args.E) {
+      // the accumulator row's expert and part: planes side by side are 32 (hi, mid,
+      // lo, zeros) or 64 rows (hi + lo, mid) apart
+      const int part = args.sets == 3 ? 0 : args.sets == 2 ? q >> 1 : q;
+      const int e = lane + (args.sets == 3 ? et * 128 + q * 32 : args.sets == 2 ? (q & 1) * 32 : 0);
+      const int col = dt * 256 + half * 128;
+      float* out = args.dw + ((size_t)(range * args.parts + part) * args.d + col) * args.E + e;
+      if (ok && e < args.E && part < args.parts) {
         // d is a multiple of 64: 64 columns or none
 #pragma unroll
         for (int c = 0; c < 128; c += 64)
@@ -459,36 +535,52 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
           }
       }
     }
-    uint8_t* stage = so + (warp - 2) * kStageOut;
+    int nt = dx0 / args.mt, mt = dx0 - nt * args.mt;
     for (int w = dx0; w < dx1 && ok; ++w) {
-      const int nt = w % args.xt, mt = w / args.xt;
+      const int row = mt * 128 + q * 32;
+      const __nv_bfloat162 back2 = __bfloat162bfloat162(
+          row + lane < args.T ? args.dl_back[row + lane] : __nv_bfloat16(0.f));
       if (!(ok = full())) break;
       const uint32_t t_addr = t_base + (uint32_t)((it & 1) * 256);
-#pragma unroll 1
-      for (int c = 0; c < 128; c += 64) {
-        uint32_t v[64];
-        tmem_ld_32x32b_x32(t_addr + c, v);
-        tmem_ld_32x32b_x32(t_addr + c + 32, v + 32);
-        tmem_ld_wait();
-        if (c == 64) release();
-        // the copy of the tile before has read the staging rows
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
+      // The factors are powers of two, so they can follow the rounding to bf16,
+      // on pairs.  A step of 32 columns loads the next one's sums before it packs its own.
+      uint32_t v[2][32];
+      tmem_ld_32x32b_x32(t_addr, v[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+      for (int n = 0; n < 4; ++n) {
+        const int col = nt * 256 + half * 128 + 32 * n;
+        uint4 f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          f[i] = col < args.d ? __ldg(reinterpret_cast<const uint4*>(args.w_back + col) + i)
+                              : make_uint4(0, 0, 0, 0);
+        tmem_ld_wait();
+        if (n < 3) tmem_ld_32x32b_x32(t_addr + 32 * (n + 1), v[(n + 1) & 1]);
+        else release();
+        // two staging buffers of 32 rows x 64 bytes: the copy before the last has read its one
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+        uint8_t* stage = so + (warp - 2) * kStageOut + (n & 1) * (kStageOut / 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t g[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
           uint32_t o[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            o[j] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * j]),
-                               __uint_as_float(v[8 * i + 2 * j + 1]));
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t* u = v[n & 1] + 8 * i + 2 * j;
+            __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(u[0]), __uint_as_float(u[1]));
+            y = __hmul2(__hmul2(y, back2), *reinterpret_cast<const __nv_bfloat162*>(&g[j]));
+            o[j] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          // 64-byte swizzle: the 16-byte column of a row XOR bits 1 and 2 of the row
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
               make_uint4(o[0], o[1], o[2], o[3]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        const int col = nt * 256 + half * 128 + c, row = mt * 128 + q * 32;
         if (lane == 0 && col < args.d && row < args.T) tma_store_2d(&tm_dx, stage, col, row);
       }
+      if (++mt == args.mt) mt = 0, ++nt;
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
@@ -501,12 +593,12 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
 }
 
 // dw = the ranges' tiles added in order (blocks [0, dw_blocks)); db = the
-// plane blocks' column sums added in fp64 (32 experts a block).
+// column sums of the dL blocks added in fp64 (8 experts a block, 32 threads each).
 __global__ void __launch_bounds__(256) k_router_sum(const float* __restrict__ part, int ranges,
                                                     long long n, float* __restrict__ dw,
                                                     int dw_blocks, const float* __restrict__ sums,
                                                     int sum_rows, int E, float* __restrict__ db) {
-  __shared__ double red[8][32];
+  __shared__ double red[32][8];
   pdl_trigger();
   pdl_wait();
   if ((int)blockIdx.x < dw_blocks) {
@@ -528,24 +620,27 @@ __global__ void __launch_bounds__(256) k_router_sum(const float* __restrict__ pa
     }
     return;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int e = ((int)blockIdx.x - dw_blocks) * 32 + lane;
+  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
+  const int e = ((int)blockIdx.x - dw_blocks) * 8 + c;
   double s = 0.0;
-  if (e < E)
-    for (int r = warp; r < sum_rows; r += 8) s += sums[(size_t)r * E + e];
-  red[warp][lane] = s;
+  if (e < E) {
+#pragma unroll 8
+    for (int r = g; r < sum_rows; r += 32) s += sums[(size_t)r * E + e];
+  }
+  red[g][c] = s;
   __syncthreads();
-  if (warp == 0 && e < E) {
+  if (g == 0 && e < E) {
     s = 0.0;
-    for (int w = 0; w < 8; ++w) s += red[w][lane];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += red[i][c];
     db[e] = (float)s;
   }
 }
 
-// bf16 tensor map of up to 4 dimensions, innermost first, 128-byte swizzle;
-// strides in bytes of dimensions 1 and up.
+// 16-bit tensor map of up to 4 dimensions, innermost first; strides in bytes of dimensions 1 and up.
 bool make_map(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
-              const uint64_t* strides, const uint32_t* box) {
+              const uint64_t* strides, const uint32_t* box,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   const auto enc = tensor_map_encoder();
   if (!enc) return false;
   cuuint64_t d[4], s[3];
@@ -553,8 +648,7 @@ bool make_map(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
   for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i];
   for (int i = 0; i + 1 < rank; ++i) s[i] = strides[i];
   return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, s, b, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
 
@@ -565,37 +659,55 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
                               const BwdLayout& L, char* ws, int sms, cudaStream_t st) {
   const int T = s.T, d = s.d, E = s.E, cp = L.cp;
   __nv_bfloat16* dlp = reinterpret_cast<__nv_bfloat16*>(ws + L.dl_planes);
-  __nv_bfloat16* wp = reinterpret_cast<__nv_bfloat16*>(ws + L.w_planes);
+  __half* dlh = reinterpret_cast<__half*>(ws + L.dl_half);
+  __half* wh = reinterpret_cast<__half*>(ws + L.w_half);
+  __nv_bfloat16* dl_back = reinterpret_cast<__nv_bfloat16*>(ws + L.dl_back);
+  __nv_bfloat16* w_back = reinterpret_cast<__nv_bfloat16*>(ws + L.w_back);
   float* sums = reinterpret_cast<float*>(ws + L.db_part);
   float* part = reinterpret_cast<float*>(ws + L.dw_part);
   const bool products = dw || dx;
   const auto vec = [&](const float* p) {
     return (int)(E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0);
   };
-  const PlanesArgs pd{dl, products ? dlp : nullptr, db ? sums : nullptr, T, E, cp, dw ? 3 : 2,
-                      L.plane_rows, (T + L.plane_rows - 1) / L.plane_rows, vec(dl)};
-  const PlanesArgs pw{w_g, wp, nullptr, d, E, cp, 2, 32, dx ? (d + 31) / 32 : 0, vec(w_g)};
-  cudaError_t e = launch_kernel(k_router_planes, dim3(pd.blocks + pw.blocks), dim3(256), 0, st, 1,
-                                pd, pw);
+  const RouterPlanes pl = router_planes(E);
+  const bool apart = pl.sets == 3;  // each plane for itself, or side by side in a row of four
+  const long long prow = apart ? pl.width : 4 * pl.width;
+  const PlanesArgs pd{dl, dw ? dlp : nullptr, dx ? dlh : nullptr, dl_back, db ? sums : nullptr,
+                      T, prow, apart ? (long long)T * pl.width : pl.width, E, cp, pl.width,
+                      !apart, L.plane_rows, (T + L.plane_rows - 1) / L.plane_rows, vec(dl)};
+  const PlanesArgs pw{w_g, nullptr, wh, w_back, nullptr, d, 0, 0, E, cp, 0, 0, 32,
+                      dx ? (d + 31) / 32 : 0, vec(w_g)};
+  const auto planes = [&](auto kern, int lanes) {
+    return launch_kernel(kern, dim3(pd.blocks + pw.blocks), dim3(256),
+                         sizeof(float) * (256 / lanes) * cp, st, 1, pd, pw);
+  };
+  cudaError_t e = cp <= 64    ? planes(k_router_planes<8, 1>, 8)
+                  : cp <= 128 ? planes(k_router_planes<16, 1>, 16)
+                  : cp <= 256 ? planes(k_router_planes<32, 1>, 32)
+                  : cp <= 512 ? planes(k_router_planes<32, 2>, 32)
+                              : planes(k_router_planes<32, 4>, 32);
   if (e != cudaSuccess) return e;
 
   const int kblocks = (T + 63) / 64, kper = router_range_blocks(s, dx != nullptr);
   const int ranges = (kblocks + kper - 1) / kper;
-  const bool direct = ranges == 1;
+  const bool direct = ranges * pl.parts == 1;
   if (products) {
     RouterGemmArgs a{};
     a.T = T, a.d = d, a.E = E;
-    a.ne = (E + 127) / 128, a.nd = (d + 255) / 256;
+    a.sets = pl.sets, a.parts = pl.parts;
+    a.ne = apart ? (E + 127) / 128 : 1, a.nd = (d + 255) / 256;
     a.kblocks = kblocks, a.kper = kper;
     a.dw_items = dw ? a.ne * a.nd * ranges : 0;
-    a.xt = (d + 255) / 256, a.kx = cp / 64;
-    a.dx_items = dx ? (T + 127) / 128 * a.xt : 0;
+    a.mt = (T + 127) / 128, a.kx = cp / 64;
+    a.dl_back = dl_back, a.w_back = w_back;
+    a.dx_items = dx ? a.mt * a.nd : 0;
     const int grid = std::min(a.dw_items + a.dx_items, sms);
     // Shares of dx: `heavy` blocks have one dW item more than the others, worth
-    // kper / kx dx items; a level n of dx items for the heavy ones gives the
-    // others n + kper / kx.
+    // `more` dx items; a level n of dx items for the heavy ones gives the others
+    // n + more.
     const int heavy = a.dw_items % grid, light = grid - heavy;
-    const double more = (double)a.kper / a.kx;
+    const double more =
+        (std::min(kper, kblocks) * router_dw_block_us(E) + 1.2) / router_dx_tile_us(E);
     const double level = std::max(0.0, (a.dx_items - light * more) / grid);
     a.light_dx = heavy == 0 ? a.dx_items
                             : (int)std::min<double>(a.dx_items, light * (level + more) + 0.5);
@@ -603,17 +715,19 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
     const uint64_t row = (uint64_t)cp * 2;
     CUtensorMap mx, mn, mk, mw, mdx;
     const uint64_t xd[3] = {64, (uint64_t)T, (uint64_t)d / 64}, xs[2] = {(uint64_t)d * 2, 128};
-    const uint64_t nd[4] = {64, (uint64_t)T, (uint64_t)cp / 64, 3}, ns[3] = {row, 128, row * T};
-    const uint64_t kd[3] = {(uint64_t)cp, (uint64_t)T, 3}, ks[2] = {row, row * T};
-    const uint64_t wd[3] = {(uint64_t)cp, (uint64_t)d, 2}, wst[2] = {row, row * d};
+    const uint64_t nd[4] = {64, (uint64_t)T, (uint64_t)prow / 64, apart ? 3u : 1u};
+    const uint64_t ns[3] = {(uint64_t)prow * 2, 128, (uint64_t)prow * 2 * T};
+    const uint64_t kd[2] = {(uint64_t)cp, (uint64_t)T}, wd[2] = {(uint64_t)cp, (uint64_t)d};
     const uint64_t od[2] = {(uint64_t)d, (uint64_t)T}, os[1] = {(uint64_t)d * 2};
-    const uint32_t xb[3] = {64, 64, 4}, nb[4] = {64, 64, 2, 1}, kb[3] = {64, 128, 1},
-                   wb[3] = {64, 256, 1}, ob[2] = {64, 32};
-    // without dW there may be no x, without dx no dx: a map of the planes, unused, stands in
-    if (!make_map(&mx, dw ? (const void*)x : dlp, 3, dw ? xd : kd, dw ? xs : ks, dw ? xb : kb) ||
-        !make_map(&mn, dlp, 4, nd, ns, nb) || !make_map(&mk, dlp, 3, kd, ks, kb) ||
-        !make_map(&mw, wp, 3, wd, wst, wb) ||
-        !make_map(&mdx, dx ? dx : dlp, dx ? 2 : 3, dx ? od : kd, dx ? os : ks, dx ? ob : kb))
+    const uint32_t xb[3] = {64, 64, 4}, nb[4] = {64, 64, 2, 1}, kb[2] = {64, 128},
+                   wb[2] = {64, 256}, ob[2] = {32, 32};
+    // without dW there may be no x, without dx no dx: an unused map of the planes stands in
+    if (!make_map(&mx, dw ? (const void*)x : dlh, dw ? 3 : 2, dw ? xd : kd, dw ? xs : &row,
+                  dw ? xb : kb) ||
+        !make_map(&mn, dlp, 4, nd, ns, nb) || !make_map(&mk, dlh, 2, kd, &row, kb) ||
+        !make_map(&mw, wh, 2, wd, &row, wb) ||
+        !make_map(&mdx, dx ? (const void*)dx : dlh, 2, dx ? od : kd, dx ? os : &row, ob,
+                  CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
     e = cudaFuncSetAttribute(k_router_gemm, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kRouterSmem);
@@ -624,10 +738,10 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
   }
   const long long n = (long long)d * E;
   const int dw_blocks = dw && !direct ? (int)std::min<long long>((n / 4 + 255) / 256, 8LL * sms) : 0;
-  const int db_blocks = db ? (E + 31) / 32 : 0;
+  const int db_blocks = db ? (E + 7) / 8 : 0;
   if (dw_blocks + db_blocks == 0) return e;
   return launch_kernel(k_router_sum, dim3(dw_blocks + db_blocks), dim3(256), 0, st, 1, part,
-                       ranges, n, dw, dw_blocks, sums, pd.blocks, E, db);
+                       ranges * pl.parts, n, dw, dw_blocks, sums, pd.blocks, E, db);
 }
 
 }  // namespace moe

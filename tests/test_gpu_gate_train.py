@@ -415,10 +415,17 @@ def check_router(T, d, E, dw=True, db=True, dx=True, seed=0, scale=1.0):
         assert bool((off <= bound + 1e-37).all()), ("dbias", float((off - bound).max()))
     if dx:
         ref = l64 @ W64.t()
-        # each product to 2^-15 (operands cut to 16 bits at least), fp32 sums that may truncate
-        n = 3 * E + 16
+        # Both operands are rounded to fp16 after a power of two brings their row's
+        # largest value to [2^14, 2^15): off by 2^-11 of the value while that is
+        # normal (2^-14 up), else by half of 2^-24, which is 2^-39 of the row's largest.
+        # A product is then off by 2^-10 + 2^-22 and the rows' 2^-39 terms.  Sums in
+        # fp32 that may truncate, two scalings back.
+        n = E + 16
         mags = l64.abs() @ W64.abs().t()
-        bound = BF16 * ref.abs() + (1 + BF16) * (2.0 ** -15 + n * 2 * U32) * mags
+        low = 2.0 ** -39 * (l64.abs().amax(1)[:, None] * W64.abs().sum(1)[None, :]
+                            + l64.abs().sum(1)[:, None] * W64.abs().amax(1)[None, :])
+        bound = BF16 * ref.abs() + (1 + BF16) * ((2.0 ** -10 + 2.0 ** -22 + n * 2 * U32) * mags
+                                                 + 1.01 * low)
         off = (out["dx"].double() - ref).abs()
         assert bool((off <= bound + 1e-37).all()), ("dx", float((off - bound).max()))
     return x, W, dl, s, ws, out
