@@ -11,6 +11,7 @@ device is not an sm_100 GPU, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -506,9 +507,20 @@ class _Operands:
         self.where, self.index = where, None
 
     def ptr(self, t, dtype, shape, name, optional=False):
+        if t is None and optional:
+            return None
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous()
+                and (shape is None or t.shape == shape)):
+            index = t.get_device()
+            if index == self.index and index >= 0:
+                return t.data_ptr()
+            if self.index is None and index >= 0:
+                self.index = index
+                return t.data_ptr()
+        self._refuse(t, dtype, shape, name)
+
+    def _refuse(self, t, dtype, shape, name):
         if t is None:
-            if optional:
-                return None
             raise TypeError(f"{self.where}: {name} is required")
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{self.where}: {name} must be a torch.Tensor")
@@ -522,13 +534,8 @@ class _Operands:
                              f"got {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{self.where}: {name} must be contiguous")
-        index = t.get_device()
-        if self.index is None:
-            self.index = index
-        elif index != self.index:
-            raise ValueError(f"{self.where}: {name} is on cuda:{index}, other tensors on "
-                             f"cuda:{self.index}")
-        return t.data_ptr()
+        raise ValueError(f"{self.where}: {name} is on cuda:{t.get_device()}, other tensors on "
+                         f"cuda:{self.index}")
 
     def workspace(self, ws, need: int):
         p = self.ptr(ws, torch.uint8, None, "ws")
@@ -537,19 +544,25 @@ class _Operands:
         return p
 
     def launch(self, fn, stream, *args):
-        if stream is not None and stream.device_index != self.index:
+        if stream is None:
+            handle = torch._C._cuda_getCurrentRawStream(self.index)
+        elif stream.device_index == self.index:
+            handle = stream.cuda_stream
+        else:
             raise ValueError(f"{self.where}: the stream is on cuda:{stream.device_index}, the "
                              f"tensors on cuda:{self.index}")
-        if self.index == torch.cuda.current_device():
-            status = fn(*args, self._stream(stream))
+        if self.index == torch._C._cuda_getDevice():
+            status = fn(*args, handle)
         else:
             with torch.cuda.device(self.index):
-                status = fn(*args, self._stream(stream))
+                status = fn(*args, handle)
         if status != MOE_OK:
             raise MoEError(status, self.where)
 
-    def _stream(self, stream):
-        return (torch.cuda.current_stream(self.index) if stream is None else stream).cuda_stream
+
+@functools.lru_cache(maxsize=1024)
+def _bwd_bytes(T, d, E, k, f, R, S) -> int:
+    return moe_workspace_size_bwd(MoEShape(T, d, E, k, f, R), S)
 
 
 def moe_workspace_size_bwd(shape: MoEShape, S: int = 1) -> int:
@@ -584,7 +597,7 @@ def moe_balance_loss(logits, idx, loss, counts, tokens, shape: MoEShape, ws, bal
     o = _Operands("moe_balance_loss")
     T, E, k = shape.T, shape.E, shape.k
     S = _seq_count(o.where, seq_offsets)
-    need = moe_workspace_size_bwd(shape, S)
+    need = _bwd_bytes(T, shape.d, E, k, shape.f, shape.R, S)
     args = (o.ptr(logits, torch.float32, (T, E), "logits"),
             o.ptr(idx, torch.int32, (T, k), "idx"),
             o.ptr(token_mask, torch.uint8, (T,), "token_mask", True),
@@ -640,7 +653,7 @@ def moe_router_bwd(x, w_g, dlogits, shape: MoEShape, ws, dw_g=None, dbias=None, 
     (T, d) bf16; each is optional (x serves dw_g alone, w_g dx alone)."""
     o = _Operands("moe_router_bwd")
     T, d, E = shape.T, shape.d, shape.E
-    need = moe_workspace_size_bwd(shape, 1)
+    need = _bwd_bytes(T, d, E, shape.k, shape.f, shape.R, 1)
     args = (o.ptr(x, torch.bfloat16, (T, d), "x", dw_g is None),
             o.ptr(w_g, torch.float32, (d, E), "w_g", dx is None),
             o.ptr(dlogits, torch.float32, (T, E), "dlogits"), ctypes.byref(shape),
@@ -681,9 +694,9 @@ class GradList:
     def _refresh(self):
         """Checks the tensors and fills the entries, unless no address has
         changed since the last time."""
-        seen = [t.data_ptr() for t in self.grads]
+        seen = list(map(torch.Tensor.data_ptr, self.grads))
         if self.outs is not self.grads:
-            seen += [t.data_ptr() for t in self.outs]
+            seen += map(torch.Tensor.data_ptr, self.outs)
         if seen == self._seen:
             return
         o = _Operands("GradList")

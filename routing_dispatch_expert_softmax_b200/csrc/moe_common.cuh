@@ -262,8 +262,11 @@ inline BwdLayout bwd_layout(const moe_shape& s, int S) {
     o = align_up(o + bytes, 256);
     return at;
   };
-  // 32 tokens a block (4 for each warp) until 592 blocks, 4 on each SM, are full
-  L.chunk = (int)(T <= 32 * 592 ? 32 : (T + 591) / 592);
+  // up to 64 tokens one block, which then needs no second kernel; else 32 tokens a
+  // block (4 for each warp) until the SMs are full, with three blocks (two above
+  // 512 experts) each
+  const long long nblk = E <= 512 ? 444 : 296;
+  L.chunk = T <= 64 ? 64 : (int)std::max(32LL, (T + nblk - 1) / nblk);
   const size_t slots = (size_t)((T + L.chunk - 1) / L.chunk) + S;
   L.prob = take(sizeof(float) * slots * E);
   L.count = take(sizeof(int) * slots * E);

@@ -16,11 +16,16 @@ namespace {
 // chunks of 4: chunk v of lane l holds the columns v * 4 * LPR + 4 l + (0..3),
 // so a group's 16-byte loads are contiguous.  Up to 128 experts a lane holds
 // 4 values and a warp 32 / LPR rows at once; above, a whole warp takes one row.
+// Each group works on kRows rows together (their shuffle chains overlap) and, up
+// to 512 experts, has the next ones' loads in flight meanwhile.
 template <int LPR, int NV>
 struct RowCfg {
   static constexpr int kLpr = LPR, kNv = NV;
   static constexpr int kGroups = 32 / LPR;  // rows of a warp at once
   static constexpr int kCols = LPR * NV;    // columns a group can hold
+  static constexpr int kRows = NV == 4 ? 4 : NV == 8 ? 2 : 1;
+  static constexpr bool kAhead = NV <= 16;
+  static constexpr int kBlocks = NV <= 16 ? 3 : 2;  // blocks of an SM
 };
 
 template <int LPR, int NV>
@@ -28,23 +33,93 @@ __device__ __forceinline__ int col_of(int l, int i) {
   return (i >> 2) * (4 * LPR) + 4 * l + (i & 3);
 }
 
-// Columns at or past E read as -inf: their exp is 0 and they never are the
-// maximum.  vec: rows are 16-byte aligned (E % 4 == 0 and the base is).
+// Two fp32 values as one 64-bit operand: the packed instructions of sm_100 do
+// two adds, products or fmas each, with the roundings of the single ones.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+constexpr f32x2 kNone = 0xff800000ff800000ull;  // a pair of -inf
+
+// A lane's NV values as pairs.  Columns at or past E read as -inf: their exp is
+// 0 and they never are the maximum.  vec: rows are 16-byte aligned (E % 4 == 0
+// and the base is).
 template <int LPR, int NV>
 __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int l, bool vec,
-                                         float (&v)[NV]) {
+                                         f32x2 (&v)[NV / 2]) {
 #pragma unroll
   for (int c = 0; c < NV / 4; ++c) {
     const int e = c * 4 * LPR + 4 * l;
     if (vec) {
-      float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (e < E) q = __ldcs(reinterpret_cast<const float4*>(row + e));
-      v[4 * c] = q.x, v[4 * c + 1] = q.y, v[4 * c + 2] = q.z, v[4 * c + 3] = q.w;
+      // as 64-bit halves: a pair made of two floats would wait for the load here
+      ulonglong2 q = make_ulonglong2(kNone, kNone);
+      if (e < E) q = __ldcs(reinterpret_cast<const ulonglong2*>(row + e));
+      v[2 * c] = q.x;
+      v[2 * c + 1] = q.y;
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * c + i] = e + i < E ? __ldcs(row + e + i) : -INFINITY;
+      v[2 * c] = pair(e < E ? __ldcs(row + e) : -INFINITY, e + 1 < E ? __ldcs(row + e + 1) : -INFINITY);
+      v[2 * c + 1] =
+          pair(e + 2 < E ? __ldcs(row + e + 2) : -INFINITY, e + 3 < E ? __ldcs(row + e + 3) : -INFINITY);
     }
   }
+}
+
+__device__ __forceinline__ float rcp_fast(float v) {  // 1 ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float log_fast(float v) {  // __logf without its care for denormals
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r * 0.6931471805599453f;
+}
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The maximum over each group of LPR lanes, NaN left aside.
+template <int LPR>
+__device__ __forceinline__ float group_max(float v) {
+  if constexpr (LPR == 32) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  }
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
 template <int LPR>
@@ -54,39 +129,69 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-template <int LPR>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
-// The row's values become exp(v - max); returns their sum and the maximum.
+// Each row's values become exp(v - max); gives their sum and the maximum.
 // live: some value is not -inf (a NaN counts: it has to show in the result).
 // A row without a live value gives exp values of 0 and a sum of 0.
-template <int LPR, int NV>
-__device__ __forceinline__ float row_exp(float (&v)[NV], float& top, bool& live) {
-  float m = -INFINITY;
-  bool some = false;
+// exp is ex2.approx of the difference times log2 e: with a difference of size D
+// off by at most (2.3 D + 4) 2^-24 of the value, and values below 2^-126 are 0.
+// These kernels are bound by their instructions, of which expf takes four times as many.
+template <int LPR, int NV, int RU>
+__device__ __forceinline__ void rows_exp(f32x2 (&v)[RU][NV / 2], float (&top)[RU],
+                                         float (&sum)[RU], bool (&live)[RU]) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    m = fmaxf(m, v[i]);
-    some |= v[i] != -INFINITY;
-  }
-  m = group_max<LPR>(m);
-  unsigned votes = __ballot_sync(0xffffffffu, some);
-  const int g0 = (threadIdx.x & 31) / LPR * LPR;
-  live = LPR == 32 ? votes != 0 : ((votes >> g0) & ((1u << (LPR & 31)) - 1u)) != 0;
-  // all -inf beside a NaN leaves m = -inf; 0 instead keeps the -inf columns at 0
-  const float sub = m == -INFINITY ? 0.f : m;
-  float s = 0.f;
+  for (int u = 0; u < RU; ++u) {
+    float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    v[i] = expf(v[i] - sub);
-    s += v[i];
+    for (int i = 0; i < NV / 2; ++i) {
+      const float2 q = unpair(v[u][i]);
+      m = max3(m, q.x, q.y);
+    }
+    top[u] = m;
   }
-  top = sub;
-  return group_sum<LPR>(s);
+#pragma unroll
+  for (int u = 0; u < RU; ++u) top[u] = group_max<LPR>(top[u]);
+#pragma unroll
+  for (int u = 0; u < RU; ++u) {
+    live[u] = top[u] != -INFINITY;
+    if (!__all_sync(0xffffffffu, live[u])) {  // nothing but -inf, and perhaps NaN
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < NV / 2; ++i) {
+        const float2 q = unpair(v[u][i]);
+        nan |= q.x != q.x || q.y != q.y;
+      }
+      const unsigned votes = __ballot_sync(0xffffffffu, nan);
+      const int g0 = (threadIdx.x & 31) / LPR * LPR;
+      const unsigned mine = LPR == 32 ? votes : (votes >> g0) & ((1u << (LPR & 31)) - 1u);
+      // with 0 in the maximum's place the -inf values keep giving 0
+      if (!live[u]) top[u] = 0.f, live[u] = mine != 0;
+    }
+    const f32x2 down = pair(-top[u], -top[u]), log2e = pair(kLog2e, kLog2e);
+    f32x2 t = 0;
+#pragma unroll
+    for (int i = 0; i < NV / 2; ++i) {
+      const float2 q = unpair(mul2(add2(v[u][i], down), log2e));
+      v[u][i] = pair(exp2_fast(q.x), exp2_fast(q.y));
+      t = i ? add2(t, v[u][i]) : v[u][i];
+    }
+    const float2 q = unpair(t);
+    sum[u] = q.x + q.y;
+  }
+  if constexpr (LPR == 32 && RU == 2) {
+    // both rows in one chain: half a warp goes on with each
+    const bool hi = (threadIdx.x & 16) != 0;
+    float t = hi ? sum[1] : sum[0];
+    t += __shfl_xor_sync(0xffffffffu, hi ? sum[0] : sum[1], 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    sum[0] = __shfl_sync(0xffffffffu, t, 0);
+    sum[1] = __shfl_sync(0xffffffffu, t, 16);
+  } else {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < RU; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
+  }
 }
 
 // The sequence s with off[s] <= t < off[s + 1] (the last such s, so an empty
@@ -117,11 +222,36 @@ struct BalancePart {
   int* n;       // [nblk + S]
 };
 
+// The loss from the sums over all counted tokens (one thread): f = the sequences'
+// sum of E / (k N^2) sum_e count prob_sum, z = the sum of lse^2.  A coefficient of
+// 0 leaves its term out, whatever the term is.
+__device__ __forceinline__ void write_loss(double f, double z, long long n, int live,
+                                           float balance_coef, float z_coef, float* loss,
+                                           int* totals) {
+  const double lb = live > 0 && balance_coef != 0.f ? balance_coef * f / live : 0.0;
+  const double lz = n > 0 && z_coef != 0.f ? z_coef * z / (double)n : 0.0;
+  loss[0] = (float)(lb + lz);
+  loss[1] = (float)lb;
+  loss[2] = (float)lz;
+  totals[0] = (int)n;
+  totals[1] = live;
+}
+
+// The results, where one block has all tokens in one sequence and finishes them
+// itself (loss == nullptr: k_balance_finish does).
+struct BalanceWhole {
+  float balance_coef, z_coef;
+  float* loss;
+  int* counts;
+  int* tokens;
+  float* prob_mean;
+};
+
 template <int LPR, int NV>
-__global__ void __launch_bounds__(256) k_balance_rows(
+__global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_balance_rows(
     const float* __restrict__ logits, const int* __restrict__ idx,
     const uint8_t* __restrict__ mask, const int* __restrict__ off, int S, int T, int E, int k,
-    int C, int vec, BalancePart part, int* err) {
+    int C, int vec, BalancePart part, int* err, const BalanceWhole whole) {
   using R = RowCfg<LPR, NV>;
   extern __shared__ float sm[];
   float* red = sm;                                        // [8][kCols]
@@ -148,56 +278,117 @@ __global__ void __launch_bounds__(256) k_balance_rows(
       ++s;
       continue;
     }
-    float acc[NV];
+    f32x2 acc[NV / 2];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) acc[i] = 0.f;
+    for (int i = 0; i < NV / 2; ++i) acc[i] = 0;
     float zacc = 0.f;
     int nacc = 0;
-    for (int r0 = t + warp * R::kGroups; r0 < end; r0 += 8 * R::kGroups) {
-      const int r = r0 + g;
-      const bool in = r < end && (!mask || mask[r]);
-      float v[NV];
-      if (in) {
-        load_row<LPR, NV>(logits + (size_t)r * E, E, l, vec, v);
-      } else {
+    constexpr int RU = R::kRows, kStep = 8 * R::kGroups * RU;
+    struct Rows {
+      f32x2 v[RU][NV / 2];
+      int id[RU];  // the lane's first selection
+      bool in[RU];
+    };
+    // rows r0 + u * kGroups + g
+    auto load = [&](Rows& q, int r0) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = -INFINITY;
+      for (int u = 0; u < RU; ++u) {
+        const int r = r0 + u * R::kGroups + g;
+        q.in[u] = r < end;
+        if (r < end) {
+          load_row<LPR, NV>(logits + (size_t)r * E, E, l, vec, q.v[u]);
+          if (l < k) q.id[u] = __ldg(idx + (size_t)r * k + l);
+          if (mask) q.in[u] = mask[r] != 0;
+        }
       }
-      float top;
-      bool live;
-      const float sum = row_exp<LPR, NV>(v, top, live);
-      if (in && live) {
-        const float inv = 1.f / sum;
+    };
+    auto count = [&](int e) {
+      if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
+      else bad_id = true;
+    };
+    auto add_rows = [&](Rows& q, int r0) {
+      float top[RU], sum[RU];
+      bool live[RU];
+      rows_exp<LPR, NV, RU>(q.v, top, sum, live);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) acc[i] += v[i] * inv;
-        if (l == 0) {
-          const float lse = top + logf(sum);
-          zacc += lse * lse;
-          ++nacc;
+      for (int u = 0; u < RU; ++u) {
+        if (!(q.in[u] && live[u])) continue;
+        const float inv = rcp_fast(sum[u]);
+        const f32x2 inv2 = pair(inv, inv);
+#pragma unroll
+        for (int i = 0; i < NV / 2; ++i) acc[i] = fma2(q.v[u][i], inv2, acc[i]);
+        const float lse = top[u] + log_fast(sum[u]);  // every lane of the group the same
+        zacc = fmaf(lse, lse, zacc);
+        ++nacc;
+        if (l < k) count(q.id[u]);
+        if (LPR < 32) {
+          const int r = r0 + u * R::kGroups + g;
+          for (int j = l + LPR; j < k; j += LPR) count(__ldg(idx + (size_t)r * k + j));
         }
-        for (int j = l; j < k; j += LPR) {
-          const int e = __ldg(idx + (size_t)r * k + j);
-          if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
-          else bad_id = true;
-        }
+      }
+    };
+    const int first = t + warp * R::kGroups * RU;
+    Rows even = {}, odd = {};
+    if constexpr (R::kAhead) {
+      if (first < end) load(even, first);
+      for (int r0 = first; r0 < end; r0 += 2 * kStep) {
+        load(odd, r0 + kStep);  // past the end: nothing is read, nothing counts
+        add_rows(even, r0);
+        if (r0 + kStep >= end) break;
+        load(even, r0 + 2 * kStep);
+        add_rows(odd, r0 + kStep);
+      }
+    } else {
+      for (int r0 = first; r0 < end; r0 += kStep) {
+        load(even, r0);
+        add_rows(even, r0);
       }
     }
     // groups of the warp, then the block's 8 warps
 #pragma unroll
     for (int o = LPR; o < 32; o <<= 1) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+      for (int i = 0; i < NV / 2; ++i)
+        acc[i] = add2(acc[i], __shfl_xor_sync(0xffffffffu, acc[i], o));
       zacc += __shfl_xor_sync(0xffffffffu, zacc, o);
       nacc += __shfl_xor_sync(0xffffffffu, nacc, o);
     }
     if (g == 0) {
 #pragma unroll
-      for (int c = 0; c < NV / 4; ++c)
+      for (int c = 0; c < NV / 4; ++c) {
+        const float2 p0 = unpair(acc[2 * c]), p1 = unpair(acc[2 * c + 1]);
         *reinterpret_cast<float4*>(red + warp * R::kCols + c * 4 * LPR + 4 * l) =
-            make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
+            make_float4(p0.x, p0.y, p1.x, p1.y);
+      }
     }
     if (lane == 0) zred[warp] = zacc, nred[warp] = nacc;
     __syncthreads();
+    if (whole.loss) {
+      double f = 0.0, z = 0.0;
+      int n = 0;
+      for (int w = 0; w < 8; ++w) z += zred[w], n += nred[w];
+      for (int e = threadIdx.x; e < E; e += 256) {
+        float p = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) p += red[w * R::kCols + e];
+        f += (double)p * hist[e];
+        whole.counts[e] = hist[e];
+        if (whole.prob_mean) whole.prob_mean[e] = n > 0 ? p / (float)n : 0.f;
+      }
+      __shared__ double fred[8];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o);
+      if (lane == 0) fred[warp] = f;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        f = 0.0;
+        for (int w = 0; w < 8; ++w) f += fred[w];
+        whole.tokens[0] = n;
+        write_loss(n > 0 ? f * E / ((double)k * n * n) : 0.0, z, n, n > 0, whole.balance_coef,
+                   whole.z_coef, whole.loss, whole.tokens + 1);
+      }
+      break;
+    }
     const size_t slot = (size_t)blockIdx.x + s;
     for (int e = threadIdx.x; e < E; e += 256) {
       float p = 0.f;
@@ -222,15 +413,17 @@ __global__ void __launch_bounds__(256) k_balance_rows(
 }
 
 // Block (x, s): 32 experts of sequence s, summed over the slots of the token
-// blocks that meet it; 8 warps take the slots in turn.  The last block to
+// blocks that meet it; W warps take the slots in turn (many warps when a
+// sequence has many slots: the sums are a chain of loads).  The last block to
 // finish (a ticket) adds the sequences' terms up in order.
-__global__ void __launch_bounds__(256) k_balance_finish(
+template <int W>
+__global__ void __launch_bounds__(32 * W) k_balance_finish(
     BalancePart part, const int* __restrict__ off, int S, int T, int E, int k, int C,
     float balance_coef, float z_coef, double* __restrict__ term, double* __restrict__ zterm,
     float* __restrict__ loss, int* __restrict__ counts, int* __restrict__ tokens,
     float* __restrict__ prob_mean, int* err, int* ticket) {
-  __shared__ double pred[8][32], zr[8];
-  __shared__ int cred[8][32], nr[8], is_last;
+  __shared__ double pred[W][32], zr[W];
+  __shared__ int cred[W][32], nr[W], is_last;
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -244,14 +437,15 @@ __global__ void __launch_bounds__(256) k_balance_finish(
   int c = 0, n = 0;
   if (b > a) {
     const int blk0 = a / C, blk1 = (b - 1) / C;
-    for (int q = blk0 + warp; q <= blk1; q += 8) {
-      const size_t slot = (size_t)q + s;
-      if (e < E) {
+    if (e < E) {
+#pragma unroll 4
+      for (int q = blk0 + warp; q <= blk1; q += W) {
+        const size_t slot = (size_t)q + s;
         p += part.prob[slot * E + e];
         c += part.count[slot * E + e];
       }
     }
-    for (int q = blk0 + (int)threadIdx.x; q <= blk1; q += 256) {
+    for (int q = blk0 + (int)threadIdx.x; q <= blk1; q += 32 * W) {
       z += part.z[q + s];
       n += part.n[q + s];
     }
@@ -268,7 +462,7 @@ __global__ void __launch_bounds__(256) k_balance_finish(
   if (warp == 0) {
     p = 0.0, c = 0, z = 0.0, n = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) p += pred[w][lane], c += cred[w][lane], z += zr[w], n += nr[w];
+    for (int w = 0; w < W; ++w) p += pred[w][lane], c += cred[w][lane], z += zr[w], n += nr[w];
     if (e < E) {
       counts[(size_t)s * E + e] = c;
       if (prob_mean) prob_mean[(size_t)s * E + e] = n > 0 ? (float)(p / n) : 0.f;
@@ -294,15 +488,15 @@ __global__ void __launch_bounds__(256) k_balance_finish(
   z = 0.0;
   long long tot = 0;
   int live = 0;
-  for (long long i = threadIdx.x; i < (long long)S * ntile; i += 256) f += __ldcg(term + i);
-  for (int i = threadIdx.x; i < S; i += 256) {
+  for (long long i = threadIdx.x; i < (long long)S * ntile; i += 32 * W) f += __ldcg(term + i);
+  for (int i = threadIdx.x; i < S; i += 32 * W) {
     const int m = __ldcg(tokens + i);
     z += __ldcg(zterm + i);
     tot += m;
     live += m > 0;
   }
-  __shared__ double fr[8];
-  __shared__ long long tr[8];
+  __shared__ double fr[W];
+  __shared__ long long tr[W];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     f += __shfl_xor_sync(0xffffffffu, f, o);
@@ -314,15 +508,8 @@ __global__ void __launch_bounds__(256) k_balance_finish(
   __syncthreads();
   if (threadIdx.x == 0) {
     f = 0.0, z = 0.0, tot = 0, live = 0;
-    for (int w = 0; w < 8; ++w) f += fr[w], z += zr[w], tot += tr[w], live += nr[w];
-    // a coefficient of 0 leaves its term out, whatever the term is
-    const double lb = live > 0 && balance_coef != 0.f ? balance_coef * f / live : 0.0;
-    const double lz = tot > 0 && z_coef != 0.f ? z_coef * z / (double)tot : 0.0;
-    loss[0] = (float)(lb + lz);
-    loss[1] = (float)lb;
-    loss[2] = (float)lz;
-    tokens[S] = (int)tot;
-    tokens[S + 1] = live;
+    for (int w = 0; w < W; ++w) f += fr[w], z += zr[w], tot += tr[w], live += nr[w];
+    write_loss(f, z, tot, live, balance_coef, z_coef, loss, tokens + S);
     *ticket = 0;
   }
 }
@@ -351,8 +538,9 @@ struct GateArgs {
 };
 
 template <int LPR, int NV>
-__global__ void __launch_bounds__(256) k_gate_bwd(const GateArgs a) {
+__global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_gate_bwd(const GateArgs a) {
   using R = RowCfg<LPR, NV>;
+  constexpr int RU = NV == 4 ? 2 : 1, kStep = R::kGroups * RU;
   extern __shared__ float sm[];
   pdl_trigger();
   pdl_wait();
@@ -365,8 +553,8 @@ __global__ void __launch_bounds__(256) k_gate_bwd(const GateArgs a) {
   __syncwarp();
   const bool aux = a.counts != nullptr;
   const long long gw = (long long)blockIdx.x * 8 + warp;
-  const long long first = gw * a.rows_per_warp;
-  const long long last = min((long long)a.T, first + a.rows_per_warp);
+  const int first = (int)min((long long)a.T, gw * a.rows_per_warp);
+  const int last = (int)min((long long)a.T, (gw + 1) * a.rows_per_warp);
   float cf = 0.f, zc = 0.f;
   int live_seqs = 1;
   if (aux) {
@@ -376,110 +564,168 @@ __global__ void __launch_bounds__(256) k_gate_bwd(const GateArgs a) {
     zc = a.z_coef != 0.f ? 2.f * a.z_coef * up / (float)max(1, tot) : 0.f;
     cf = a.balance_coef * up;
   }
-  float f[NV];
+  f32x2 f[NV / 2];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) f[i] = 0.f;
+  for (int i = 0; i < NV / 2; ++i) f[i] = 0;
   int seq = -2, seq_end = -1;  // [.., seq_end) is the run whose f is loaded
   bool bad_id = false;
-  for (long long r0 = first; r0 < last; r0 += R::kGroups) {
-    const int t = (int)(r0 + g);
-    const bool in = r0 + g < last;
-    float v[NV], sum = 0.f, top = 0.f;
-    bool live = false;
-    if (aux) {
-      bool use = in && (!a.mask || a.mask[t]);
-      if (in && t >= seq_end) {
-        seq = a.off ? find_seq(a.off, a.S, t) : 0;
-        const bool real = seq >= 0 && seq < a.S;
-        seq_end = !a.off || seq >= a.S ? a.T : __ldg(a.off + seq + 1);
-        if (real && cf != 0.f) {
-          const int n = max(1, __ldg(a.tokens + seq));
-          const float per =
-              cf * (float)a.E / ((float)live_seqs * (float)a.k * (float)n * (float)n);
+  struct Rows {
+    f32x2 v[RU][NV / 2];
+    float w[RU], dw[RU];  // the lane's first slot
+    int id[RU];
+    bool in[RU];
+  };
+  // rows r0 + u * kGroups + g: logits and the lane's first slot
+  auto load = [&](Rows& q, int r0) {
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int e = col_of<LPR, NV>(l, i);
-            f[i] = e < a.E ? per * (float)__ldg(a.counts + (size_t)seq * a.E + e) : 0.f;
+    for (int u = 0; u < RU; ++u) {
+      const int t = r0 + u * R::kGroups + g;
+      q.in[u] = t < last;
+      q.id[u] = -1;
+      q.w[u] = q.dw[u] = 0.f;
+      if (t < last) {
+        if (aux) {
+          load_row<LPR, NV>(a.logits + (size_t)t * a.E, a.E, l, a.vec, q.v[u]);
+          if (a.mask) q.in[u] = a.mask[t] != 0;
+        }
+        if (a.dw && l < a.k) {
+          const size_t at = (size_t)t * a.k + l;
+          q.id[u] = __ldg(a.idx + at);
+          q.w[u] = __ldg(a.w + at);
+          q.dw[u] = __ldg(a.dw + at);
+        }
+      }
+    }
+  };
+  auto grad_rows = [&](Rows& q, int r0) {
+    if (aux) {
+      float top[RU], sum[RU], dot[RU], add[RU];
+      bool live[RU];
+      rows_exp<LPR, NV, RU>(q.v, top, sum, live);
+#pragma unroll
+      for (int u = 0; u < RU; ++u) {
+        const int t = r0 + u * R::kGroups + g;
+        if (t < last && t >= seq_end) {
+          seq = a.off ? find_seq(a.off, a.S, t) : 0;
+          const bool real = seq >= 0 && seq < a.S;
+          seq_end = !a.off || seq >= a.S ? a.T : __ldg(a.off + seq + 1);
+          if (real && cf != 0.f) {
+            const int n = max(1, __ldg(a.tokens + seq));
+            const float per =
+                cf * (float)a.E / ((float)live_seqs * (float)a.k * (float)n * (float)n);
+            const int* c = a.counts + (size_t)seq * a.E;
+#pragma unroll
+            for (int i = 0; i < NV / 2; ++i) {
+              const int e = col_of<LPR, NV>(l, 2 * i);
+              f[i] = pair(e < a.E ? per * (float)__ldg(c + e) : 0.f,
+                          e + 1 < a.E ? per * (float)__ldg(c + e + 1) : 0.f);
+            }
           }
         }
-      }
-      use = use && seq >= 0 && seq < a.S;
-      if (use) {
-        load_row<LPR, NV>(a.logits + (size_t)t * a.E, a.E, l, a.vec, v);
-      } else {
+        live[u] = live[u] && q.in[u] && seq >= 0 && seq < a.S;
+        const float inv = rcp_fast(sum[u]);
+        const f32x2 inv2 = pair(inv, inv);
+        f32x2 d = 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = -INFINITY;
-      }
-      sum = row_exp<LPR, NV>(v, top, live);
-      live = live && use;
-      float dot = 0.f;
-      const float inv = 1.f / sum;
+        for (int i = 0; i < NV / 2; ++i) {
+          q.v[u][i] = mul2(q.v[u][i], inv2);
+          d = i ? fma2(f[i], q.v[u][i], d) : mul2(f[i], q.v[u][i]);
+        }
+        const float2 h = unpair(d);
+        dot[u] = group_sum<LPR>(h.x + h.y);
+        add[u] = (zc != 0.f ? zc * (top[u] + log_fast(sum[u])) : 0.f) - dot[u];
+        const f32x2 add2x = pair(add[u], add[u]);
+        if (live[u]) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        v[i] *= inv;
-        dot = fmaf(f[i], v[i], dot);
-      }
-      dot = group_sum<LPR>(dot);
-      const float add = (zc != 0.f ? zc * (top + logf(sum)) : 0.f) - dot;
+          for (int i = 0; i < NV / 2; ++i) q.v[u][i] = mul2(q.v[u][i], add2(f[i], add2x));
+        } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = live ? v[i] * (f[i] + add) : 0.f;
+          for (int i = 0; i < NV / 2; ++i) q.v[u][i] = 0;
+        }
+      }
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[i] = 0.f;
-    }
-    if (a.dw) {
-      float dotw = 0.f;
-      if (in)
-        for (int j = l; j < a.k; j += LPR)
-          dotw = fmaf(__ldg(a.w + (size_t)t * a.k + j), __ldg(a.dw + (size_t)t * a.k + j), dotw);
-      dotw = group_sum<LPR>(dotw);
-      // A step adds the slots j0 .. j0 + LPR - 1.  Ids are distinct in a token;
-      // should two slots of a step share one, the lower slot goes first.
-      for (int j0 = 0; j0 < a.k; j0 += LPR) {
-        const int j = j0 + l;
-        int e = -1;
-        float add = 0.f;
-        if (in && j < a.k) {
-          const size_t at = (size_t)t * a.k + j;
-          e = __ldg(a.idx + at);
-          if (e < 0 || e >= a.E) e = -1, bad_id = true;
-          const float wj = __ldg(a.w + at);
-          add = wj * (__ldg(a.dw + at) - dotw);
-        }
-        const unsigned same = __match_any_sync(0xffffffffu, e < 0 ? -1 - lane : g * a.E + e);
-        const int before = __popc(same & ((1u << lane) - 1u));
-        int most = before;
+      for (int u = 0; u < RU; ++u)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-        for (int turn = 0; turn <= most; ++turn) {
-          if (e >= 0 && before == turn) grow[e] += add;
+        for (int i = 0; i < NV / 2; ++i) q.v[u][i] = 0;
+    }
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      const int t = r0 + u * R::kGroups + g;
+      const bool in = t < last;
+      if (a.dw) {
+        float dotw = q.w[u] * q.dw[u];
+        if (LPR < 32 && in)
+          for (int j = l + LPR; j < a.k; j += LPR)
+            dotw = fmaf(__ldg(a.w + (size_t)t * a.k + j), __ldg(a.dw + (size_t)t * a.k + j), dotw);
+        dotw = group_sum<LPR>(dotw);
+        // A step adds the slots j0 .. j0 + LPR - 1.  Ids are distinct in a token;
+        // should two slots of a step share one, the lower slot goes first.
+        for (int j0 = 0; j0 < a.k; j0 += LPR) {
+          const int j = j0 + l;
+          int e = q.id[u];
+          float wj = q.w[u], dwj = q.dw[u];
+          if (LPR < 32 && j0 > 0 && in && j < a.k) {
+            const size_t at = (size_t)t * a.k + j;
+            e = __ldg(a.idx + at), wj = __ldg(a.w + at), dwj = __ldg(a.dw + at);
+          }
+          if (!(in && j < a.k)) e = -1;
+          else if (e < 0 || e >= a.E) e = -1, bad_id = true;
+          const float term = wj * (dwj - dotw);
+          const unsigned same = __match_any_sync(0xffffffffu, e < 0 ? -1 - lane : g * a.E + e);
+          const int before = __popc(same & ((1u << lane) - 1u));
+          for (int turn = 0; __any_sync(0xffffffffu, before >= turn); ++turn) {
+            if (e >= 0 && before == turn) grow[e] += term;
+            __syncwarp();
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < NV / 4; ++c) {
+          float4* at = reinterpret_cast<float4*>(grow + c * 4 * LPR + 4 * l);
+          const float4 more = *at;
+          q.v[u][2 * c] = add2(q.v[u][2 * c], pair(more.x, more.y));
+          q.v[u][2 * c + 1] = add2(q.v[u][2 * c + 1], pair(more.z, more.w));
+          if (LPR < 32) *at = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        __syncwarp();
+        if (LPR == 32) {  // k <= 32: one slot a lane
+          if ((unsigned)q.id[u] < (unsigned)a.E) grow[q.id[u]] = 0.f;
           __syncwarp();
         }
       }
+      if (in) {
+        float* out = a.dlogits + (size_t)t * a.E;
 #pragma unroll
-      for (int c = 0; c < NV / 4; ++c) {
-        float4* q = reinterpret_cast<float4*>(grow + c * 4 * LPR + 4 * l);
-        const float4 add = *q;
-        v[4 * c] += add.x, v[4 * c + 1] += add.y, v[4 * c + 2] += add.z, v[4 * c + 3] += add.w;
-        *q = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      __syncwarp();
-    }
-    if (in) {
-      float* out = a.dlogits + (size_t)t * a.E;
-#pragma unroll
-      for (int c = 0; c < NV / 4; ++c) {
-        const int e = c * 4 * LPR + 4 * l;
-        if (a.vec) {
-          if (e < a.E)
-            __stcs(reinterpret_cast<float4*>(out + e),
-                   make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (e + i < a.E) __stcs(out + e + i, v[4 * c + i]);
+        for (int c = 0; c < NV / 4; ++c) {
+          const int e = c * 4 * LPR + 4 * l;
+          const float2 o0 = unpair(q.v[u][2 * c]), o1 = unpair(q.v[u][2 * c + 1]);
+          if (a.vec) {
+            if (e < a.E)
+              __stcs(reinterpret_cast<float4*>(out + e), make_float4(o0.x, o0.y, o1.x, o1.y));
+          } else {
+            if (e < a.E) __stcs(out + e, o0.x);
+            if (e + 1 < a.E) __stcs(out + e + 1, o0.y);
+            if (e + 2 < a.E) __stcs(out + e + 2, o1.x);
+            if (e + 3 < a.E) __stcs(out + e + 3, o1.y);
+          }
         }
       }
+    }
+  };
+  Rows even = {}, odd = {};
+  if constexpr (R::kAhead) {
+    if (first < last) load(even, first);
+    for (int r0 = first; r0 < last; r0 += 2 * kStep) {
+      load(odd, r0 + kStep);  // past the end: nothing is read or written
+      grad_rows(even, r0);
+      if (r0 + kStep >= last) break;
+      load(even, r0 + 2 * kStep);
+      grad_rows(odd, r0 + kStep);
+    }
+  } else {
+    for (int r0 = first; r0 < last; r0 += kStep) {
+      load(even, r0);
+      grad_rows(even, r0);
     }
   }
   if (bad_id) record_error(a.err, MOE_ERR_DEVICE_CHECK, 42);
@@ -587,18 +833,24 @@ cudaError_t launch_balance_loss(const float* logits, const int* idx, const uint8
   int* err = reinterpret_cast<int*>(ws);
   const int vec = s.E % 4 == 0 && aligned16(logits);
   const int C = L.chunk, nblk = (s.T + C - 1) / C;
+  const bool one = nblk == 1 && !off;
+  const BalanceWhole whole{balance_coef, z_coef, one ? loss : nullptr, counts, tokens, prob_mean};
   cudaError_t e = with_rows(s.E, [&](auto cfg) {
     using R = decltype(cfg);
     const size_t smem = sizeof(float) * 8 * R::kCols + sizeof(int) * s.E;
     return launch_kernel(k_balance_rows<R::kLpr, R::kNv>, dim3(nblk), dim3(256), smem, st, 1,
-                         logits, idx, mask, off, S, s.T, s.E, s.k, C, vec, part, err);
+                         logits, idx, mask, off, S, s.T, s.E, s.k, C, vec, part, err, whole);
   });
-  if (e != cudaSuccess) return e;
-  return launch_kernel(k_balance_finish, dim3((s.E + 31) / 32, S), dim3(256), 0, st, 1, part, off,
-                       S, s.T, s.E, s.k, C, balance_coef, z_coef,
-                       reinterpret_cast<double*>(ws + L.term),
-                       reinterpret_cast<double*>(ws + L.zterm), loss, counts, tokens, prob_mean,
-                       err, err + kBalanceTicket);
+  if (e != cudaSuccess || one) return e;
+  const auto finish = [&](auto kern, int warps) {
+    return launch_kernel(kern, dim3((s.E + 31) / 32, S), dim3(32 * warps), 0, st, 1, part, off, S,
+                         s.T, s.E, s.k, C, balance_coef, z_coef,
+                         reinterpret_cast<double*>(ws + L.term),
+                         reinterpret_cast<double*>(ws + L.zterm), loss, counts, tokens, prob_mean,
+                         err, err + kBalanceTicket);
+  };
+  // 4 warps for sequences of up to 16 blocks on average, else 32
+  return nblk <= 16 * S ? finish(k_balance_finish<4>, 4) : finish(k_balance_finish<32>, 32);
 }
 
 cudaError_t launch_gate_bwd(const float* logits, const int* idx, const float* w, const float* dw,
@@ -611,8 +863,8 @@ cudaError_t launch_gate_bwd(const float* logits, const int* idx, const float* w,
              S, s.T, s.E, s.k, 1, vec, err};
   return with_rows(s.E, [&](auto cfg) {
     using R = decltype(cfg);
-    // Runs of rows: enough warps for 8 blocks an SM, whole groups of rows each.
-    const long long warps = 64LL * sms;
+    // Runs of rows for two rounds of the blocks that an SM holds, whole groups each.
+    const long long warps = 16LL * R::kBlocks * sms;
     long long rows = (s.T + warps - 1) / warps;
     rows = (rows + R::kGroups - 1) / R::kGroups * R::kGroups;
     a.rows_per_warp = (int)rows;

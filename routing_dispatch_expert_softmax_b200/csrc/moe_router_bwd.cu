@@ -17,6 +17,8 @@
 // adds the ranges' partial tiles in order.
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "moe_kernels.cuh"
 
 namespace moe {
@@ -262,8 +264,7 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, ui
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, const void* src, int c0,
                                              int c1) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
-      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(tm)),
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(tm)),
       "r"(smem_u32(src)), "r"(c0), "r"(c1)
       : "memory");
 }
@@ -578,7 +579,11 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0 && col < args.d && row < args.T) tma_store_2d(&tm_dx, stage, col, row);
+        if (lane == 0) {
+          if (col < args.d && row < args.T) tma_store_2d(&tm_dx, stage, col, row);
+          // a group for every step, stored or not: the waits above count steps
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
       }
       if (++mt == args.mt) mt = 0, ++nt;
     }
@@ -713,7 +718,7 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
                             : (int)std::min<double>(a.dx_items, light * (level + more) + 0.5);
     a.dw = direct ? dw : part, a.err = reinterpret_cast<int*>(ws);
     const uint64_t row = (uint64_t)cp * 2;
-    CUtensorMap mx, mn, mk, mw, mdx;
+    CUtensorMap mx{}, mn{}, mk{}, mw{}, mdx{};
     const uint64_t xd[3] = {64, (uint64_t)T, (uint64_t)d / 64}, xs[2] = {(uint64_t)d * 2, 128};
     const uint64_t nd[4] = {64, (uint64_t)T, (uint64_t)prow / 64, apart ? 3u : 1u};
     const uint64_t ns[3] = {(uint64_t)prow * 2, 128, (uint64_t)prow * 2 * T};
@@ -721,17 +726,22 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
     const uint64_t od[2] = {(uint64_t)d, (uint64_t)T}, os[1] = {(uint64_t)d * 2};
     const uint32_t xb[3] = {64, 64, 4}, nb[4] = {64, 64, 2, 1}, kb[2] = {64, 128},
                    wb[2] = {64, 256}, ob[2] = {32, 32};
-    // without dW there may be no x, without dx no dx: an unused map of the planes stands in
-    if (!make_map(&mx, dw ? (const void*)x : dlh, dw ? 3 : 2, dw ? xd : kd, dw ? xs : &row,
-                  dw ? xb : kb) ||
-        !make_map(&mn, dlp, 4, nd, ns, nb) || !make_map(&mk, dlh, 2, kd, &row, kb) ||
-        !make_map(&mw, wh, 2, wd, &row, wb) ||
-        !make_map(&mdx, dx ? (const void*)dx : dlh, 2, dx ? od : kd, dx ? os : &row, ob,
-                  CU_TENSOR_MAP_SWIZZLE_64B))
+    // only the maps that the items use (another's bytes are never read)
+    if (dw && (!make_map(&mx, x, 3, xd, xs, xb) || !make_map(&mn, dlp, 4, nd, ns, nb)))
       return cudaErrorInvalidValue;
-    e = cudaFuncSetAttribute(k_router_gemm, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kRouterSmem);
-    if (e != cudaSuccess) return e;
+    if (dx && (!make_map(&mk, dlh, 2, kd, &row, kb) || !make_map(&mw, wh, 2, wd, &row, wb) ||
+               !make_map(&mdx, dx, 2, od, os, ob, CU_TENSOR_MAP_SWIZZLE_64B)))
+      return cudaErrorInvalidValue;
+    // Once for each device: the attribute belongs to the device's copy of the kernel.
+    static std::atomic<uint64_t> ready[2];
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if (dev >= 128 || !(ready[dev / 64].load(std::memory_order_acquire) >> (dev % 64) & 1)) {
+      e = cudaFuncSetAttribute(k_router_gemm, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kRouterSmem);
+      if (e != cudaSuccess) return e;
+      if (dev < 128) ready[dev / 64].fetch_or(1ull << (dev % 64), std::memory_order_release);
+    }
     e = launch_kernel(k_router_gemm, dim3(grid), dim3(kRouterThreads), kRouterSmem, st, 1, mx, mn,
                       mk, mw, mdx, a);
     if (e != cudaSuccess) return e;
