@@ -1,45 +1,61 @@
 // The global norm of a list of gradients and their clipping by it.
 //
 // The list goes to the kernels by value, as a launch parameter: nothing is
-// uploaded, so the calls allocate nothing and can be captured.  Tensors are
-// cut into chunks of equal length and the blocks stride over the chunks of all
-// tensors, whatever the tensors' sizes.
+// uploaded, so the calls allocate nothing and can be captured.  The tensors'
+// elements count as one sequence in units of 2048 (a tensor's last unit may be
+// shorter).  The sequence is cut into equal rounds, and every block takes an equal
+// run of each: the blocks end together whatever the tensors' sizes, and those that
+// run at the same time read neighbouring memory (one long run for each block took
+// 15% longer where the scaling streams from and to HBM).
 #include "moe_kernels.cuh"
 
 namespace moe {
 
 namespace {
 
+constexpr int kUnit = 2048;       // elements
+constexpr int kPiece = 32;        // most units of a block's run in one round
+constexpr int kGradTable = 256;   // tensors of one launch
+constexpr int kGradBlocks = 592;  // blocks of one launch (partial sums), 4 for each SM
+
 struct GradEntry {
   const void* in;
   void* out;
   long long n;
-  int chunk0;   // the chunks of the tensors before this one
-  int in_bf16;  // 0: fp32
+  long long unit0;  // the units of the tensors before this one
+  int in_bf16;      // 0: fp32
   int out_bf16;
-  int pad;
 };
 
-template <int N>
 struct GradTable {
-  GradEntry e[N];
-  int count;   // entries
-  int chunks;  // chunks of all entries
-  int chunk;   // elements of a chunk, a multiple of 8
+  GradEntry e[kGradTable];
+  int count;        // entries
+  long long units;  // of all entries
 };
 
-constexpr int kGradTable = 256;   // tensors of one launch
-constexpr int kGradBlocks = 592;  // blocks of one launch (partial sums)
-
-template <int N>
-__device__ __forceinline__ const GradEntry& entry_of(const GradTable<N>& t, int c) {
+__device__ __forceinline__ const GradEntry& entry_of(const GradTable& t, long long u) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (t.e[mid].chunk0 <= c) lo = mid;
+    if (t.e[mid].unit0 <= u) lo = mid;
     else hi = mid - 1;
   }
   return t.e[lo];
+}
+
+// Rounds of the sequence, and the units [first, last) of this block's run in one.
+__device__ __forceinline__ long long rounds_of(const GradTable& t) {
+  return (t.units + (long long)gridDim.x * kPiece - 1) / ((long long)gridDim.x * kPiece);
+}
+__device__ __forceinline__ void run_of(const GradTable& t, long long round, long long rounds,
+                                       long long& first, long long& last) {
+  const long long r0 = t.units * round / rounds, n = t.units * (round + 1) / rounds - r0;
+  first = r0 + n * blockIdx.x / gridDim.x;
+  last = r0 + n * (blockIdx.x + 1) / gridDim.x;
+}
+
+__device__ __forceinline__ long long units_of(const GradEntry& e) {
+  return (e.n + kUnit - 1) / kUnit;
 }
 
 __device__ __forceinline__ float widen(float v) { return v; }
@@ -72,8 +88,28 @@ __device__ __forceinline__ int head_of(const T* p, long long n) {
   return (int)min((long long)h, n);
 }
 
-// The sum of squares of n elements: products and sums in fp64, which neither
-// overflow nor vanish for any fp32 value.
+// The squares of a 16-byte vector (4 or 8 elements) are summed in fp32, off by at
+// most 8 2^-24 of their sum, and added up in fp64: converting every element makes
+// the pass three times as long (fp64 conversions bound it).  A vector whose sum is
+// outside [1e-30, 1e38], where squares pass fp32's range or lose bits in it, is
+// summed in fp64 after all, so no fp32 value overflows or vanishes.
+template <class T>
+__device__ __forceinline__ double vec_squares(const Vec16<T>& v) {
+  constexpr int N = Vec16<T>::kN;
+  float f[N];
+  v.get(f);
+  float s = f[0] * f[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) s = fmaf(f[i], f[i], s);
+  if (s >= 1e-30f && s <= 1e38f) return s;
+  double d = 0.0;
+  if ((v.raw.x | v.raw.y | v.raw.z | v.raw.w) != 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) d = fma((double)f[i], (double)f[i], d);
+  }
+  return d;
+}
+
 template <class T>
 __device__ double sum_squares(const T* __restrict__ p, int n) {
   double s = 0.0;
@@ -82,23 +118,24 @@ __device__ double sum_squares(const T* __restrict__ p, int n) {
     const double v = widen(p[threadIdx.x]);
     s += v * v;
   }
-  constexpr int N = Vec16<T>::kN, U = 4;
+  constexpr int N = Vec16<T>::kN, U = 8;
   const int nv = (n - h) / N;
   const uint4* q = reinterpret_cast<const uint4*>(p + h);
-  for (int i0 = threadIdx.x; i0 < nv; i0 += 256 * U) {
+  int i = threadIdx.x;
+  for (; i + 256 * (U - 1) < nv; i += 256 * U) {
     Vec16<T> v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      v[u].raw = make_uint4(0, 0, 0, 0);
-      if (i0 + 256 * u < nv) v[u].raw = __ldg(q + i0 + 256 * u);
-    }
+    for (int u = 0; u < U; ++u) v[u].raw = __ldg(q + i + 256 * u);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float f[N];
-      v[u].get(f);
+    for (int u = 0; u < U; ++u) s += vec_squares(v[u]);
+  }
+  if (i < nv) {
+    Vec16<T> v[U];
 #pragma unroll
-      for (int i = 0; i < N; ++i) s = fma((double)f[i], (double)f[i], s);
-    }
+    for (int u = 0; u < U; ++u)
+      v[u].raw = i + 256 * u < nv ? __ldg(q + i + 256 * u) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += vec_squares(v[u]);
   }
   const int at = h + nv * N + (int)threadIdx.x;
   if (at < n) {
@@ -110,8 +147,7 @@ __device__ double sum_squares(const T* __restrict__ p, int n) {
 
 // Block partials of this launch go to partial[first ...]; the last block of
 // the list's last launch (done != nullptr) adds up all of them in order.
-template <int N>
-__global__ void __launch_bounds__(256) k_grad_sumsq(const __grid_constant__ GradTable<N> t,
+__global__ void __launch_bounds__(256) k_grad_sumsq(const __grid_constant__ GradTable t,
                                                     double* __restrict__ partial, int first,
                                                     double* __restrict__ sumsq, int last_launch,
                                                     unsigned* __restrict__ ticket) {
@@ -120,12 +156,19 @@ __global__ void __launch_bounds__(256) k_grad_sumsq(const __grid_constant__ Grad
   pdl_trigger();
   pdl_wait();
   double s = 0.0;
-  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const GradEntry& e = entry_of(t, c);
-    const long long at = (long long)(c - e.chunk0) * t.chunk;
-    const int n = (int)min((long long)t.chunk, e.n - at);
-    s += e.in_bf16 ? sum_squares(static_cast<const __nv_bfloat16*>(e.in) + at, n)
-                   : sum_squares(static_cast<const float*>(e.in) + at, n);
+  const long long rounds = rounds_of(t);
+  for (long long round = 0; round < rounds; ++round) {
+    long long u, last;
+    run_of(t, round, rounds, u, last);
+    while (u < last) {
+      const GradEntry& e = entry_of(t, u);
+      const long long end = min(last, e.unit0 + units_of(e));
+      const long long at = (u - e.unit0) * kUnit;
+      const int n = (int)(min((end - e.unit0) * kUnit, e.n) - at);
+      s += e.in_bf16 ? sum_squares(static_cast<const __nv_bfloat16*>(e.in) + at, n)
+                     : sum_squares(static_cast<const float*>(e.in) + at, n);
+      u = end;
+    }
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
@@ -171,39 +214,77 @@ __device__ __forceinline__ void put16(__nv_bfloat16* p, const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7])));
 }
 
-template <class TI, class TO>
-__device__ void scale(const TI* in, TO* out, int n, float c) {
-  constexpr int N = Vec16<TI>::kN, U = 4;
-  const int h = head_of(in, n);
-  if ((reinterpret_cast<uintptr_t>(out + h) & 15) != 0) {
-    for (int i = threadIdx.x; i < n; i += 256) put(out + i, c * widen(in[i]));
-    return;
-  }
-  if ((int)threadIdx.x < h) put(out + threadIdx.x, c * widen(in[threadIdx.x]));
-  const int nv = (n - h) / N;
-  const uint4* q = reinterpret_cast<const uint4*>(in + h);
-  TO* o = out + h;
-  for (int i0 = threadIdx.x; i0 < nv; i0 += 256 * U) {
-    Vec16<TI> v[U];
+// 16 bytes from byte m (0 .. 14, even) of the 32 bytes lo, hi.
+__device__ __forceinline__ uint4 window16(uint4 lo, uint4 hi, int m) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t t[6], u[5];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + 256 * u < nv) v[u].raw = __ldcs(q + i0 + 256 * u);
+  for (int i = 0; i < 6; ++i) t[i] = m & 8 ? w[i + 2] : w[i];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (i0 + 256 * u >= nv) break;
-      float f[N];
-      v[u].get(f);
-#pragma unroll
-      for (int i = 0; i < N; ++i) f[i] *= c;
-      put16(o + (size_t)(i0 + 256 * u) * N, f);
-    }
-  }
-  const int at = h + nv * N + (int)threadIdx.x;
-  if (at < n) put(out + at, c * widen(in[at]));
+  for (int i = 0; i < 5; ++i) u[i] = m & 4 ? t[i + 1] : t[i];
+  const int sh = (m & 2) * 8;
+  return make_uint4(__funnelshift_r(u[0], u[1], sh), __funnelshift_r(u[1], u[2], sh),
+                    __funnelshift_r(u[2], u[3], sh), __funnelshift_r(u[3], u[4], sh));
 }
 
-template <int N>
-__global__ void __launch_bounds__(256) k_grad_scale(const __grid_constant__ GradTable<N> t,
+// out[i] = c in[i] for a piece's n elements; [lo, hi) are the bytes of the whole
+// tensor.  Stores are 16 bytes at 16-byte boundaries of out; where in lies
+// otherwise, its elements come from two aligned loads that stay inside the tensor
+// (a gradient of odd length shifts all that follow it in a flat buffer).
+template <class TI, class TO>
+__device__ void scale(const TI* in, TO* out, int n, float c, const char* lo, const char* hi) {
+  constexpr int N = Vec16<TI>::kN, U = 4;
+  int h = head_of(out, n);
+  const int m = (int)(reinterpret_cast<uintptr_t>(in + h) & 15);
+  const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(in + h) - m);
+  int nv = (n - h) / N;
+  if (m) {
+    // the first and the last vectors whose loads would leave the tensor go one by one
+    if (nv > 0 && reinterpret_cast<const char*>(q) < lo) h += N, ++q, --nv;
+    if (nv > 0 && reinterpret_cast<const char*>(q + nv + 1) > hi) --nv;
+  }
+  TO* o = out + h;
+  for (int i = threadIdx.x; i < h; i += 256) put(out + i, c * widen(in[i]));
+  // all loads of a step before its first store
+  auto store = [&](Vec16<TI> v, int i) {
+    float f[N];
+    v.get(f);
+#pragma unroll
+    for (int k = 0; k < N; ++k) f[k] *= c;
+    put16(o + (size_t)i * N, f);
+  };
+  int i = threadIdx.x;
+  if (m) {
+    for (; i + 256 * (U - 1) < nv; i += 256 * U) {
+      uint4 a[U], b[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) a[u] = __ldg(q + i + 256 * u), b[u] = __ldg(q + i + 256 * u + 1);
+#pragma unroll
+      for (int u = 0; u < U; ++u) store(Vec16<TI>{window16(a[u], b[u], m)}, i + 256 * u);
+    }
+    for (; i < nv; i += 256) store(Vec16<TI>{window16(__ldg(q + i), __ldg(q + i + 1), m)}, i);
+  } else {
+    for (; i + 256 * (U - 1) < nv; i += 256 * U) {
+      uint4 a[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) a[u] = __ldcs(q + i + 256 * u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) store(Vec16<TI>{a[u]}, i + 256 * u);
+    }
+    if (i < nv) {
+      uint4 a[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        a[u] = i + 256 * u < nv ? __ldcs(q + i + 256 * u) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i + 256 * u < nv) store(Vec16<TI>{a[u]}, i + 256 * u);
+    }
+  }
+  for (int at = h + nv * N + (int)threadIdx.x; at < n; at += 256) put(out + at, c * widen(in[at]));
+}
+
+__global__ void __launch_bounds__(256) k_grad_scale(const __grid_constant__ GradTable t,
                                                     const double* __restrict__ sumsq,
                                                     float max_norm, float* __restrict__ norm) {
   pdl_trigger();
@@ -212,51 +293,47 @@ __global__ void __launch_bounds__(256) k_grad_scale(const __grid_constant__ Grad
   float c = 1.f;
   if (isfinite(nrm)) c = (float)fmin(1.0, (double)max_norm / (nrm + 1e-6));
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = (float)nrm;
-  // The last chunks first: the norm's pass read them last, so L2 still holds them.
-  for (int r = blockIdx.x; r < t.chunks; r += gridDim.x) {
-    const int q = t.chunks - 1 - r;
-    const GradEntry& e = entry_of(t, q);
-    if (c == 1.f && e.in == e.out) continue;
-    const long long at = (long long)(q - e.chunk0) * t.chunk;
-    const int n = (int)min((long long)t.chunk, e.n - at);
-    if (!e.in_bf16)
-      scale(static_cast<const float*>(e.in) + at, static_cast<float*>(e.out) + at, n, c);
-    else if (e.out_bf16)
-      scale(static_cast<const __nv_bfloat16*>(e.in) + at, static_cast<__nv_bfloat16*>(e.out) + at,
-            n, c);
-    else
-      scale(static_cast<const __nv_bfloat16*>(e.in) + at, static_cast<float*>(e.out) + at, n, c);
+  // The last rounds first: the norm's pass read them last, so L2 still holds them.
+  const long long rounds = rounds_of(t);
+  for (long long round = rounds - 1; round >= 0; --round) {
+    long long u, last;
+    run_of(t, round, rounds, u, last);
+    while (u < last) {
+      const GradEntry& e = entry_of(t, u);
+      const long long end = min(last, e.unit0 + units_of(e));
+      const long long at = (u - e.unit0) * kUnit;
+      const int n = (int)(min((end - e.unit0) * kUnit, e.n) - at);
+      u = end;
+      if (c == 1.f && e.in == e.out) continue;
+      const char* lo = static_cast<const char*>(e.in);
+      const char* hi = lo + e.n * (e.in_bf16 ? 2 : 4);
+      const float* f32 = static_cast<const float*>(e.in) + at;
+      const __nv_bfloat16* b16 = static_cast<const __nv_bfloat16*>(e.in) + at;
+      if (!e.in_bf16)
+        scale(f32, static_cast<float*>(e.out) + at, n, c, lo, hi);
+      else if (e.out_bf16)
+        scale(b16, static_cast<__nv_bfloat16*>(e.out) + at, n, c, lo, hi);
+      else
+        scale(b16, static_cast<float*>(e.out) + at, n, c, lo, hi);
+    }
   }
-}
-
-// Elements of a chunk: about eight chunks for each of 592 blocks, so that the
-// blocks end together, between 2048 and 65536.
-int chunk_elems(const moe_grad* g, int n) {
-  long long total = 0;
-  for (int i = 0; i < n; ++i) total += g[i].n;
-  const long long c = (total / (8 * kGradBlocks) + 2047) / 2048 * 2048;
-  return (int)std::max(2048LL, std::min(65536LL, c));
 }
 
 // Calls fn(table, grid, launch index, is the last) for each 256 tensors.
 template <class F>
 cudaError_t for_tables(const moe_grad* g, int n, F&& fn) {
-  const int chunk = chunk_elems(g, n);
   const int launches = std::max(1, (n + kGradTable - 1) / kGradTable);
   for (int q = 0; q < launches; ++q) {
-    GradTable<kGradTable> t;
+    GradTable t;
     t.count = 0;
-    t.chunk = chunk;
-    long long chunks = 0;
+    t.units = 0;
     for (int i = q * kGradTable; i < std::min(n, (q + 1) * kGradTable); ++i) {
       if (g[i].n == 0) continue;
-      t.e[t.count++] = GradEntry{g[i].data, g[i].out, g[i].n, (int)chunks,
-                                 g[i].dtype == MOE_GRAD_BF16, g[i].out_dtype == MOE_GRAD_BF16, 0};
-      chunks += (g[i].n + chunk - 1) / chunk;
+      t.e[t.count++] = GradEntry{g[i].data, g[i].out, g[i].n, t.units,
+                                 g[i].dtype == MOE_GRAD_BF16, g[i].out_dtype == MOE_GRAD_BF16};
+      t.units += (g[i].n + kUnit - 1) / kUnit;
     }
-    if (chunks > INT_MAX / 2) return cudaErrorInvalidValue;
-    t.chunks = (int)chunks;
-    const int grid = (int)std::max(1LL, std::min<long long>(chunks, kGradBlocks));
+    const int grid = (int)std::max(1LL, std::min<long long>(t.units, kGradBlocks));
     const cudaError_t e = fn(t, grid, q, q == launches - 1);
     if (e != cudaSuccess) return e;
   }
@@ -279,8 +356,8 @@ cudaError_t launch_grad_sumsq(const moe_grad* g, int n, double* sumsq, void* ws,
   double* partial = reinterpret_cast<double*>(static_cast<char*>(ws) + 512);
   unsigned* ticket = static_cast<unsigned*>(ws) + kGradTicket;
   int first = 0;
-  return for_tables(g, n, [&](const GradTable<kGradTable>& t, int grid, int, bool last) {
-    const cudaError_t e = launch_kernel(k_grad_sumsq<kGradTable>, dim3(grid), dim3(256), 0, st, 1,
+  return for_tables(g, n, [&](const GradTable& t, int grid, int, bool last) {
+    const cudaError_t e = launch_kernel(k_grad_sumsq, dim3(grid), dim3(256), 0, st, 1,
                                         t, partial, first, sumsq, (int)last, ticket);
     first += grid;
     return e;
@@ -289,8 +366,8 @@ cudaError_t launch_grad_sumsq(const moe_grad* g, int n, double* sumsq, void* ws,
 
 cudaError_t launch_grad_scale(const moe_grad* g, int n, const double* sumsq, float max_norm,
                               float* norm, cudaStream_t st) {
-  return for_tables(g, n, [&](const GradTable<kGradTable>& t, int grid, int q, bool) {
-    return launch_kernel(k_grad_scale<kGradTable>, dim3(grid), dim3(256), 0, st, 1, t, sumsq,
+  return for_tables(g, n, [&](const GradTable& t, int grid, int q, bool) {
+    return launch_kernel(k_grad_scale, dim3(grid), dim3(256), 0, st, 1, t, sumsq,
                          max_norm, q == 0 ? norm : nullptr);
   });
 }
