@@ -211,30 +211,37 @@ struct BwdLayout {
 // operand: above 64 experts a plane of its own each (three MMAs for each K step);
 // up to 64, side by side in rows of (hi | mid | lo | 0) x 64 (two MMAs); up to
 // 32, of x 32 (one).  Side by side, a plane's rows of the product are apart, so a
-// tile is `parts` partial weight gradients.
+// tile is `parts` partial weight gradients, and a kernel has to add them: up to 256
+// tokens that costs more (2.5 us) than the MMAs.
 struct RouterPlanes {
   int sets, parts, width;  // MMAs for each K step; partials; columns of one plane
 };
-inline RouterPlanes router_planes(int E) {
-  if (E <= 32) return {1, 3, 32};
-  if (E <= 64) return {2, 2, 64};
+inline RouterPlanes router_planes(int E, int T) {
+  if (E <= 32 && T > 256) return {1, 3, 32};
+  if (E <= 64 && T > 256) return {2, 2, 64};
   return {3, 1, (int)((E + 63) / 64 * 64)};
 }
 
-// Times in us that the router's backward plans with (1.85 GHz, 6.5 TB/s over 148
-// SMs): a 64-token block of a 128 x 256 tile of dW, MMAs or the 32 KB of x; a 128 x
-// 256 tile of dx, MMAs or about its 64 KB of output.
-inline double router_dw_block_us(int E) { return std::max(0.28 * router_planes(E).sets, 0.74); }
-inline double router_dx_tile_us(int E) { return std::max(0.28 * ((E + 63) / 64), 1.2); }
+// Times in us that the router's backward plans with, as measured: a 64-token block
+// of a 128 x 256 tile of dW (the MMAs, or for one set the 32 KB of x); a 128 x 256
+// tile of dx (its 64 KB of output; from 256 experts on the MMAs, and above that W's
+// tiles too, which the shared memory then does not keep); an item's start and end.
+inline double router_dw_block_us(int sets) {
+  return sets == 3 ? 1.1 : sets == 2 ? 0.85 : 0.68;
+}
+inline double router_dx_tile_us(int E) {
+  const int kx = (E + 63) / 64;
+  return kx <= 4 ? std::max(1.5, 0.5 * kx) : 0.62 * kx;
+}
+constexpr double kRouterItemUs = 2.0;
 
 // The tokens of dW are cut into ranges: more of them fill the SMs, but each
 // writes partials that are read again.  The time of `r` ranges: all work over
-// 148 SMs, but no less than the longest SM's dW items (each with 1.2 us of
-// start and end), plus each partial's way to L2 and back.  The r with the least
+// 148 SMs, but no less than the longest SM's dW items, plus each partial's way to L2 and back.  The r with the least
 // time is taken; what is returned is the 64-token blocks of one range.
 inline int router_range_blocks(const moe_shape& s, bool dx) {
-  const RouterPlanes pl = router_planes(s.E);
-  const double kb = router_dw_block_us(s.E);
+  const RouterPlanes pl = router_planes(s.E, s.T);
+  const double kb = router_dw_block_us(pl.sets);
   const long long cols = (s.d + 255) / 256;
   const long long tiles = cols * (pl.sets == 3 ? (s.E + 127) / 128 : 1);
   const long long blocks = ((long long)s.T + 63) / 64;
@@ -245,8 +252,8 @@ inline int router_range_blocks(const moe_shape& s, bool dx) {
   for (long long r = 1; r <= std::min(blocks, 148LL); ++r) {
     const long long per = (blocks + r - 1) / r, n = (blocks + per - 1) / per;
     const double waves = (double)((tiles * n + 147) / 148);
-    const double us = std::max(waves * (per * kb + 1.2),
-                               (tiles * (blocks * kb + n * 1.2) + dx_us) / 148) +
+    const double us = std::max(waves * (per * kb + kRouterItemUs),
+                               (tiles * (blocks * kb + n * kRouterItemUs) + dx_us) / 148) +
                       n * partial_us;
     if (r == 1 || us < least) best = per, least = us;
   }
@@ -263,9 +270,9 @@ inline BwdLayout bwd_layout(const moe_shape& s, int S) {
     return at;
   };
   // up to 64 tokens one block, which then needs no second kernel; else 32 tokens a
-  // block (4 for each warp) until the SMs are full, with three blocks (two above
-  // 512 experts) each
-  const long long nblk = E <= 512 ? 444 : 296;
+  // block (4 for each warp) until the SMs are full, with four blocks (three above
+  // 256 experts, two above 512) each
+  const long long nblk = E <= 256 ? 592 : E <= 512 ? 444 : 296;
   L.chunk = T <= 64 ? 64 : (int)std::max(32LL, (T + nblk - 1) / nblk);
   const size_t slots = (size_t)((T + L.chunk - 1) / L.chunk) + S;
   L.prob = take(sizeof(float) * slots * E);
@@ -277,8 +284,9 @@ inline BwdLayout bwd_layout(const moe_shape& s, int S) {
   const size_t balance = o;
   o = 256;
   L.cp = (int)align_up(E, 64);
-  L.plane_rows = (int)std::max(32LL, (T + 591) / 592);
-  const RouterPlanes pl = router_planes(s.E);
+  // up to 64 tokens one block, whose column sums need no second kernel
+  L.plane_rows = T <= 64 ? 64 : (int)std::max(32LL, (T + 591) / 592);
+  const RouterPlanes pl = router_planes(s.E, s.T);
   L.dl_planes = take(2 * (size_t)T * pl.width * (pl.sets == 3 ? 3 : 4));
   L.dl_half = take(2 * (size_t)T * L.cp);
   L.w_half = take(2 * (size_t)d * L.cp);

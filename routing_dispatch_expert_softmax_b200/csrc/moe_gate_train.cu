@@ -23,9 +23,9 @@ struct RowCfg {
   static constexpr int kLpr = LPR, kNv = NV;
   static constexpr int kGroups = 32 / LPR;  // rows of a warp at once
   static constexpr int kCols = LPR * NV;    // columns a group can hold
-  static constexpr int kRows = NV == 4 ? 4 : NV == 8 ? 2 : 1;
+  static constexpr int kRows = NV == 4 ? 2 : 1;
   static constexpr bool kAhead = NV <= 16;
-  static constexpr int kBlocks = NV <= 16 ? 3 : 2;  // blocks of an SM
+  static constexpr int kBlocks = NV <= 8 ? 4 : NV <= 16 ? 3 : 2;  // blocks of an SM
 };
 
 template <int LPR, int NV>
@@ -33,6 +33,8 @@ __device__ __forceinline__ int col_of(int l, int i) {
   return (i >> 2) * (4 * LPR) + 4 * l + (i & 3);
 }
 
+// Element offsets below are 32-bit: T E <= 2^30.
+//
 // Two fp32 values as one 64-bit operand: the packed instructions of sm_100 do
 // two adds, products or fmas each, with the roundings of the single ones.
 typedef unsigned long long f32x2;
@@ -129,7 +131,8 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Each row's values become exp(v - max); gives their sum and the maximum.
+// Each row's values become exp(v - max); gives the lane's sum of them (rows_sum and
+// sum3 add the group's up) and the row's maximum.
 // live: some value is not -inf (a NaN counts: it has to show in the result).
 // A row without a live value gives exp values of 0 and a sum of 0.
 // exp is ex2.approx of the difference times log2 e: with a difference of size D
@@ -177,6 +180,11 @@ __device__ __forceinline__ void rows_exp(f32x2 (&v)[RU][NV / 2], float (&top)[RU
     const float2 q = unpair(t);
     sum[u] = q.x + q.y;
   }
+}
+
+// Each row's sum over its group of lanes.
+template <int LPR, int RU>
+__device__ __forceinline__ void rows_sum(float (&sum)[RU]) {
   if constexpr (LPR == 32 && RU == 2) {
     // both rows in one chain: half a warp goes on with each
     const bool hi = (threadIdx.x & 16) != 0;
@@ -191,6 +199,30 @@ __device__ __forceinline__ void rows_exp(f32x2 (&v)[RU][NV / 2], float (&top)[RU
     for (int o = LPR / 2; o > 0; o >>= 1)
 #pragma unroll
       for (int u = 0; u < RU; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
+  }
+}
+
+// Three sums over each group of lanes; a whole warp does them in one chain, a
+// quarter of it each, with 9 shuffles in place of 15.
+template <int LPR>
+__device__ __forceinline__ void sum3(float& a, float& b, float& c) {
+  if constexpr (LPR == 32) {
+    const bool hi = (threadIdx.x & 16) != 0, odd = (threadIdx.x & 8) != 0;
+    float x = (hi ? c : a) + __shfl_xor_sync(0xffffffffu, hi ? a : c, 16);
+    float y = b + __shfl_xor_sync(0xffffffffu, b, 16);
+    x = (odd ? y : x) + __shfl_xor_sync(0xffffffffu, odd ? x : y, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    a = __shfl_sync(0xffffffffu, x, 0);
+    b = __shfl_sync(0xffffffffu, x, 8);
+    c = __shfl_sync(0xffffffffu, x, 16);
+  } else {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+      c += __shfl_xor_sync(0xffffffffu, c, o);
+    }
   }
 }
 
@@ -296,8 +328,8 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_balance_rows(
         const int r = r0 + u * R::kGroups + g;
         q.in[u] = r < end;
         if (r < end) {
-          load_row<LPR, NV>(logits + (size_t)r * E, E, l, vec, q.v[u]);
-          if (l < k) q.id[u] = __ldg(idx + (size_t)r * k + l);
+          load_row<LPR, NV>(logits + (unsigned)(r * E), E, l, vec, q.v[u]);
+          if (l < k) q.id[u] = __ldg(idx + (unsigned)(r * k + l));
           if (mask) q.in[u] = mask[r] != 0;
         }
       }
@@ -310,6 +342,7 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_balance_rows(
       float top[RU], sum[RU];
       bool live[RU];
       rows_exp<LPR, NV, RU>(q.v, top, sum, live);
+      rows_sum<LPR, RU>(sum);
 #pragma unroll
       for (int u = 0; u < RU; ++u) {
         if (!(q.in[u] && live[u])) continue;
@@ -585,11 +618,11 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_gate_bwd(cons
       q.w[u] = q.dw[u] = 0.f;
       if (t < last) {
         if (aux) {
-          load_row<LPR, NV>(a.logits + (size_t)t * a.E, a.E, l, a.vec, q.v[u]);
+          load_row<LPR, NV>(a.logits + (unsigned)(t * a.E), a.E, l, a.vec, q.v[u]);
           if (a.mask) q.in[u] = a.mask[t] != 0;
         }
         if (a.dw && l < a.k) {
-          const size_t at = (size_t)t * a.k + l;
+          const unsigned at = t * a.k + l;
           q.id[u] = __ldg(a.idx + at);
           q.w[u] = __ldg(a.w + at);
           q.dw[u] = __ldg(a.dw + at);
@@ -598,13 +631,13 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_gate_bwd(cons
     }
   };
   auto grad_rows = [&](Rows& q, int r0) {
-    if (aux) {
-      float top[RU], sum[RU], dot[RU], add[RU];
-      bool live[RU];
-      rows_exp<LPR, NV, RU>(q.v, top, sum, live);
+    float top[RU], sum[RU] = {}, dot[RU] = {}, dotw[RU];
+    bool live[RU] = {};
+    if (aux) rows_exp<LPR, NV, RU>(q.v, top, sum, live);
 #pragma unroll
-      for (int u = 0; u < RU; ++u) {
-        const int t = r0 + u * R::kGroups + g;
+    for (int u = 0; u < RU; ++u) {
+      const int t = r0 + u * R::kGroups + g;
+      if (aux) {
         if (t < last && t >= seq_end) {
           seq = a.off ? find_seq(a.off, a.S, t) : 0;
           const bool real = seq >= 0 && seq < a.S;
@@ -623,59 +656,57 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_gate_bwd(cons
           }
         }
         live[u] = live[u] && q.in[u] && seq >= 0 && seq < a.S;
-        const float inv = rcp_fast(sum[u]);
-        const f32x2 inv2 = pair(inv, inv);
-        f32x2 d = 0;
+        f32x2 d = mul2(f[0], q.v[u][0]);
 #pragma unroll
-        for (int i = 0; i < NV / 2; ++i) {
-          q.v[u][i] = mul2(q.v[u][i], inv2);
-          d = i ? fma2(f[i], q.v[u][i], d) : mul2(f[i], q.v[u][i]);
-        }
+        for (int i = 1; i < NV / 2; ++i) d = fma2(f[i], q.v[u][i], d);
         const float2 h = unpair(d);
-        dot[u] = group_sum<LPR>(h.x + h.y);
-        add[u] = (zc != 0.f ? zc * (top[u] + log_fast(sum[u])) : 0.f) - dot[u];
-        const f32x2 add2x = pair(add[u], add[u]);
-        if (live[u]) {
-#pragma unroll
-          for (int i = 0; i < NV / 2; ++i) q.v[u][i] = mul2(q.v[u][i], add2(f[i], add2x));
-        } else {
-#pragma unroll
-          for (int i = 0; i < NV / 2; ++i) q.v[u][i] = 0;
-        }
+        dot[u] = h.x + h.y;
       }
-    } else {
+      dotw[u] = q.w[u] * q.dw[u];
+      if (LPR < 32 && a.dw && t < last)
+        for (int j = l + LPR; j < a.k; j += LPR)
+          dotw[u] = fmaf(__ldg(a.w + (unsigned)(t * a.k + j)), __ldg(a.dw + (unsigned)(t * a.k + j)),
+                         dotw[u]);
+      sum3<LPR>(sum[u], dot[u], dotw[u]);
+      if (aux && live[u]) {
+        // v / sum (f + zc lse - dot / sum)
+        const float inv = rcp_fast(sum[u]);
+        const float add =
+            inv * ((zc != 0.f ? zc * (top[u] + log_fast(sum[u])) : 0.f) - dot[u] * inv);
+        const f32x2 inv2 = pair(inv, inv), add2x = pair(add, add);
 #pragma unroll
-      for (int u = 0; u < RU; ++u)
+        for (int i = 0; i < NV / 2; ++i) q.v[u][i] = mul2(q.v[u][i], fma2(f[i], inv2, add2x));
+      } else {
 #pragma unroll
         for (int i = 0; i < NV / 2; ++i) q.v[u][i] = 0;
+      }
     }
 #pragma unroll
     for (int u = 0; u < RU; ++u) {
       const int t = r0 + u * R::kGroups + g;
       const bool in = t < last;
       if (a.dw) {
-        float dotw = q.w[u] * q.dw[u];
-        if (LPR < 32 && in)
-          for (int j = l + LPR; j < a.k; j += LPR)
-            dotw = fmaf(__ldg(a.w + (size_t)t * a.k + j), __ldg(a.dw + (size_t)t * a.k + j), dotw);
-        dotw = group_sum<LPR>(dotw);
         // A step adds the slots j0 .. j0 + LPR - 1.  Ids are distinct in a token;
         // should two slots of a step share one, the lower slot goes first.
         for (int j0 = 0; j0 < a.k; j0 += LPR) {
-          const int j = j0 + l;
           int e = q.id[u];
           float wj = q.w[u], dwj = q.dw[u];
-          if (LPR < 32 && j0 > 0 && in && j < a.k) {
-            const size_t at = (size_t)t * a.k + j;
-            e = __ldg(a.idx + at), wj = __ldg(a.w + at), dwj = __ldg(a.dw + at);
+          if (LPR < 32 && j0 > 0) {
+            e = -1;
+            if (in && j0 + l < a.k) {
+              const unsigned at = t * a.k + j0 + l;
+              e = __ldg(a.idx + at), wj = __ldg(a.w + at), dwj = __ldg(a.dw + at);
+            }
           }
-          if (!(in && j < a.k)) e = -1;
-          else if (e < 0 || e >= a.E) e = -1, bad_id = true;
-          const float term = wj * (dwj - dotw);
-          const unsigned same = __match_any_sync(0xffffffffu, e < 0 ? -1 - lane : g * a.E + e);
+          if (in && j0 + l < a.k && (unsigned)e >= (unsigned)a.E) bad_id = true;
+          const bool has = (unsigned)e < (unsigned)a.E;
+          const float term = wj * (dwj - dotw[u]);
+          const unsigned same = __match_any_sync(0xffffffffu, has ? g * a.E + e : -1 - lane);
           const int before = __popc(same & ((1u << lane) - 1u));
-          for (int turn = 0; __any_sync(0xffffffffu, before >= turn); ++turn) {
-            if (e >= 0 && before == turn) grow[e] += term;
+          if (has && before == 0) grow[e] = LPR < 32 ? grow[e] + term : term;
+          __syncwarp();
+          for (int turn = 1; __any_sync(0xffffffffu, before >= turn); ++turn) {
+            if (has && before == turn) grow[e] += term;
             __syncwarp();
           }
         }
@@ -694,7 +725,7 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_gate_bwd(cons
         }
       }
       if (in) {
-        float* out = a.dlogits + (size_t)t * a.E;
+        float* out = a.dlogits + (unsigned)(t * a.E);
 #pragma unroll
         for (int c = 0; c < NV / 4; ++c) {
           const int e = c * 4 * LPR + 4 * l;
@@ -863,8 +894,9 @@ cudaError_t launch_gate_bwd(const float* logits, const int* idx, const float* w,
              S, s.T, s.E, s.k, 1, vec, err};
   return with_rows(s.E, [&](auto cfg) {
     using R = decltype(cfg);
-    // Runs of rows for two rounds of the blocks that an SM holds, whole groups each.
-    const long long warps = 16LL * R::kBlocks * sms;
+    // One run of whole groups for each warp that the SMs hold (two or four rounds of
+    // shorter runs: 3% and 10% slower at 131072 x 256).
+    const long long warps = 8LL * R::kBlocks * sms;
     long long rows = (s.T + warps - 1) / warps;
     rows = (rows + R::kGroups - 1) / R::kGroups * R::kGroups;
     a.rows_per_warp = (int)rows;

@@ -321,6 +321,11 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  if (warp == 0 && lane == 0) {
+    if (args.dw_items) prefetch_tensormap(&tm_x), prefetch_tensormap(&tm_dl_mn);
+    if (args.dx_items)
+      prefetch_tensormap(&tm_dl_k), prefetch_tensormap(&tm_w), prefetch_tensormap(&tm_dx);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -537,10 +542,26 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
       }
     }
     int nt = dx0 / args.mt, mt = dx0 - nt * args.mt;
+    // The factors stay in registers: the columns' as long as the items go down one
+    // block of them, the row's loaded an item ahead.
+    auto row_back = [&](int m) {
+      const int r = m * 128 + q * 32 + lane;
+      return r < args.T ? args.dl_back[r] : __nv_bfloat16(0.f);
+    };
+    __nv_bfloat16 next_back = row_back(mt);
+    uint4 f[16];
     for (int w = dx0; w < dx1 && ok; ++w) {
+      if (w == dx0 || mt == 0) {
+        const int col = nt * 256 + half * 128;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)  // 64 columns or none
+          f[i] = col + 8 * i < args.d
+                     ? __ldg(reinterpret_cast<const uint4*>(args.w_back + col) + i)
+                     : make_uint4(0, 0, 0, 0);
+      }
       const int row = mt * 128 + q * 32;
-      const __nv_bfloat162 back2 = __bfloat162bfloat162(
-          row + lane < args.T ? args.dl_back[row + lane] : __nv_bfloat16(0.f));
+      const __nv_bfloat162 back2 = __bfloat162bfloat162(next_back);
+      next_back = row_back(mt + 1 == args.mt ? 0 : mt + 1);
       if (!(ok = full())) break;
       const uint32_t t_addr = t_base + (uint32_t)((it & 1) * 256);
       // The factors are powers of two, so they can follow the rounding to bf16,
@@ -550,11 +571,6 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         const int col = nt * 256 + half * 128 + 32 * n;
-        uint4 f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          f[i] = col < args.d ? __ldg(reinterpret_cast<const uint4*>(args.w_back + col) + i)
-                              : make_uint4(0, 0, 0, 0);
         tmem_ld_wait();
         if (n < 3) tmem_ld_32x32b_x32(t_addr + 32 * (n + 1), v[(n + 1) & 1]);
         else release();
@@ -564,7 +580,8 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
         uint8_t* stage = so + (warp - 2) * kStageOut + (n & 1) * (kStageOut / 2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t g[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
+          const uint4 fi = f[4 * n + i];
+          const uint32_t g[4] = {fi.x, fi.y, fi.z, fi.w};
           uint32_t o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -674,12 +691,14 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
   const auto vec = [&](const float* p) {
     return (int)(E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0);
   };
-  const RouterPlanes pl = router_planes(E);
+  const RouterPlanes pl = router_planes(E, T);
   const bool apart = pl.sets == 3;  // each plane for itself, or side by side in a row of four
   const long long prow = apart ? pl.width : 4 * pl.width;
-  const PlanesArgs pd{dl, dw ? dlp : nullptr, dx ? dlh : nullptr, dl_back, db ? sums : nullptr,
-                      T, prow, apart ? (long long)T * pl.width : pl.width, E, cp, pl.width,
-                      !apart, L.plane_rows, (T + L.plane_rows - 1) / L.plane_rows, vec(dl)};
+  const int sum_rows = (T + L.plane_rows - 1) / L.plane_rows;
+  // one block's column sums are db itself
+  const PlanesArgs pd{dl, dw ? dlp : nullptr, dx ? dlh : nullptr, dl_back,
+                      !db ? nullptr : sum_rows == 1 ? db : sums, T, prow, apart ? (long long)T * pl.width : pl.width, E, cp, pl.width,
+                      !apart, L.plane_rows, sum_rows, vec(dl)};
   const PlanesArgs pw{w_g, nullptr, wh, w_back, nullptr, d, 0, 0, E, cp, 0, 0, 32,
                       dx ? (d + 31) / 32 : 0, vec(w_g)};
   const auto planes = [&](auto kern, int lanes) {
@@ -712,7 +731,7 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
     // n + more.
     const int heavy = a.dw_items % grid, light = grid - heavy;
     const double more =
-        (std::min(kper, kblocks) * router_dw_block_us(E) + 1.2) / router_dx_tile_us(E);
+        (std::min(kper, kblocks) * router_dw_block_us(pl.sets) + kRouterItemUs) / router_dx_tile_us(E);
     const double level = std::max(0.0, (a.dx_items - light * more) / grid);
     a.light_dx = heavy == 0 ? a.dx_items
                             : (int)std::min<double>(a.dx_items, light * (level + more) + 0.5);
@@ -748,10 +767,10 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
   }
   const long long n = (long long)d * E;
   const int dw_blocks = dw && !direct ? (int)std::min<long long>((n / 4 + 255) / 256, 8LL * sms) : 0;
-  const int db_blocks = db ? (E + 7) / 8 : 0;
+  const int db_blocks = db && sum_rows > 1 ? (E + 7) / 8 : 0;
   if (dw_blocks + db_blocks == 0) return e;
   return launch_kernel(k_router_sum, dim3(dw_blocks + db_blocks), dim3(256), 0, st, 1, part,
-                       ranges * pl.parts, n, dw, dw_blocks, sums, pd.blocks, E, db);
+                       ranges * pl.parts, n, dw, dw_blocks, sums, sum_rows, E, db);
 }
 
 }  // namespace moe

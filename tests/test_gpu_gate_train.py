@@ -193,7 +193,7 @@ def test_sequences(T, E, k, seqs, masked):
 
 @pytest.mark.parametrize("T,E,k,S", [(20000, 16, 2, 1), (20000, 16, 2, 700), (19000, 128, 4, 1)])
 def test_many_tokens(T, E, k, S):
-    # more tokens than 32 for each of 444 blocks: longer blocks
+    # more tokens than 32 for each of 592 blocks: longer blocks
     r = np.random.default_rng(1)
     seqs = None if S == 1 else np.concatenate([[0], np.sort(r.integers(0, T, S - 1)), [T - 5]])
     b = Batch(T, E, k, seqs=seqs, masked=True, seed=2).device()
