@@ -21,3 +21,4 @@ from .binding import (EXPORTS, MOE_STAGE_EVENTS, STAGE_NAMES, MOE_ERR_CUDA, MOE_
                       moe_gate_bwd, moe_combine_bwd, moe_router_bwd, GradList, moe_grad_sumsq,
                       moe_grad_scale, moe_clip_grads)
 from .layer import MoELayer  # noqa: F401
+from .gate import GateGrads, GateTrainer  # noqa: F401
