@@ -452,6 +452,7 @@ def test_router_bwd_parts(which):
 
 def test_router_bwd_tiny_and_huge_gradients():
     check_router(100, 64, 16, scale=1e-30)
+    check_router(300, 192, 40, scale=3e-34)
     check_router(100, 64, 16, scale=1e30)
 
 
