@@ -235,6 +235,13 @@ inline double router_dx_tile_us(int E) {
 }
 constexpr double kRouterItemUs = 2.0;
 
+// Adding up a partial costs its share of L2's bandwidth and a step of a chain of loads
+// (eight of them at a time from 16 partials on).
+inline double router_partial_us(const moe_shape& s, int parts, long long ranges) {
+  const long long n = parts * ranges;
+  return 8.0 * n * s.d * s.E / 5e6 + (n > 1 ? 2.5 : 0.0) + 0.1 * (n < 16 ? n : n / 8.0);
+}
+
 // The tokens of dW are cut into ranges: more of them fill the SMs, but each
 // writes partials that are read again.  The time of `r` ranges: all work over
 // 148 SMs, but no less than the longest SM's dW items, plus each partial's way to L2 and back.  The r with the least
@@ -246,7 +253,6 @@ inline int router_range_blocks(const moe_shape& s, bool dx) {
   const long long tiles = cols * (pl.sets == 3 ? (s.E + 127) / 128 : 1);
   const long long blocks = ((long long)s.T + 63) / 64;
   const double dx_us = dx ? (double)((s.T + 127) / 128) * cols * router_dx_tile_us(s.E) : 0.0;
-  const double partial_us = 8.0 * pl.parts * s.d * s.E / 5e6;  // written and read at 5 TB/s
   long long best = std::max(1LL, blocks);
   double least = 0.0;
   for (long long r = 1; r <= std::min(blocks, 148LL); ++r) {
@@ -254,7 +260,7 @@ inline int router_range_blocks(const moe_shape& s, bool dx) {
     const double waves = (double)((tiles * n + 147) / 148);
     const double us = std::max(waves * (per * kb + kRouterItemUs),
                                (tiles * (blocks * kb + n * kRouterItemUs) + dx_us) / 148) +
-                      n * partial_us;
+                      router_partial_us(s, pl.parts, n);
     if (r == 1 || us < least) best = per, least = us;
   }
   return (int)best;
@@ -269,11 +275,13 @@ inline BwdLayout bwd_layout(const moe_shape& s, int S) {
     o = align_up(o + bytes, 256);
     return at;
   };
-  // up to 64 tokens one block, which then needs no second kernel; else 32 tokens a
-  // block (4 for each warp) until the SMs are full, with four blocks (three above
-  // 256 experts, two above 512) each
+  // One sequence of up to 64 tokens: one block, which then needs no second kernel.
+  // Else 32 tokens a block (4 for each warp), or the tokens of an average sequence (a
+  // block takes the sequences in its tokens one after the other), until the SMs are
+  // full, with four blocks (three above 256 experts, two above 512) each.
   const long long nblk = E <= 256 ? 592 : E <= 512 ? 444 : 296;
-  L.chunk = T <= 64 ? 64 : (int)std::max(32LL, (T + nblk - 1) / nblk);
+  const long long least = std::min(32LL, std::max(1LL, T / S));
+  L.chunk = S == 1 && T <= 64 ? 64 : (int)std::max(least, (T + nblk - 1) / nblk);
   const size_t slots = (size_t)((T + L.chunk - 1) / L.chunk) + S;
   L.prob = take(sizeof(float) * slots * E);
   L.count = take(sizeof(int) * slots * E);

@@ -5,6 +5,8 @@
 // parallelism on 8xH200", section "Routing imbalance") but give no loss; the
 // one here is the usual product of each expert's share of the selections and
 // its mean probability, with the mean squared logsumexp beside it.
+#include <type_traits>
+
 #include "moe_kernels.cuh"
 
 namespace moe {
@@ -12,15 +14,17 @@ namespace moe {
 namespace {
 
 // ---------------------------------------------------------------- row layout
-// A group of LPR lanes owns one row of E fp32 logits, NV values a lane in
-// chunks of 4: chunk v of lane l holds the columns v * 4 * LPR + 4 l + (0..3),
-// so a group's 16-byte loads are contiguous.  Up to 128 experts a lane holds
+// A group of LPR lanes owns one row of E fp32 logits, NV values a lane: in chunks
+// of 4, chunk c of lane l the columns c * 4 * LPR + 4 l + (0..3), so that a group's
+// 16-byte loads are contiguous; or, where rows are not 16-byte aligned, value i the
+// column i * LPR + l, so that its 4-byte loads are (VEC = false).  Up to 128 experts a lane holds
 // 4 values and a warp 32 / LPR rows at once; above, a whole warp takes one row.
 // Each group works on kRows rows together (their shuffle chains overlap) and, up
 // to 512 experts, has the next ones' loads in flight meanwhile.
-template <int LPR, int NV>
+template <int LPR, int NV, bool VEC>
 struct RowCfg {
   static constexpr int kLpr = LPR, kNv = NV;
+  static constexpr bool kVec = VEC;
   static constexpr int kGroups = 32 / LPR;  // rows of a warp at once
   static constexpr int kCols = LPR * NV;    // columns a group can hold
   static constexpr int kRows = NV == 4 ? 2 : 1;
@@ -28,9 +32,9 @@ struct RowCfg {
   static constexpr int kBlocks = NV <= 8 ? 4 : NV <= 16 ? 3 : 2;  // blocks of an SM
 };
 
-template <int LPR, int NV>
+template <int LPR, bool VEC>
 __device__ __forceinline__ int col_of(int l, int i) {
-  return (i >> 2) * (4 * LPR) + 4 * l + (i & 3);
+  return VEC ? (i >> 2) * (4 * LPR) + 4 * l + (i & 3) : i * LPR + l;
 }
 
 // Element offsets below are 32-bit: T E <= 2^30.
@@ -72,24 +76,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 constexpr f32x2 kNone = 0xff800000ff800000ull;  // a pair of -inf
 
 // A lane's NV values as pairs.  Columns at or past E read as -inf: their exp is
-// 0 and they never are the maximum.  vec: rows are 16-byte aligned (E % 4 == 0
-// and the base is).
-template <int LPR, int NV>
-__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int l, bool vec,
+// 0 and they never are the maximum.
+template <int LPR, int NV, bool VEC>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int l,
                                          f32x2 (&v)[NV / 2]) {
+  if constexpr (VEC) {
 #pragma unroll
-  for (int c = 0; c < NV / 4; ++c) {
-    const int e = c * 4 * LPR + 4 * l;
-    if (vec) {
+    for (int c = 0; c < NV / 4; ++c) {
+      const int e = c * 4 * LPR + 4 * l;
       // as 64-bit halves: a pair made of two floats would wait for the load here
       ulonglong2 q = make_ulonglong2(kNone, kNone);
       if (e < E) q = __ldcs(reinterpret_cast<const ulonglong2*>(row + e));
       v[2 * c] = q.x;
       v[2 * c + 1] = q.y;
-    } else {
-      v[2 * c] = pair(e < E ? __ldcs(row + e) : -INFINITY, e + 1 < E ? __ldcs(row + e + 1) : -INFINITY);
-      v[2 * c + 1] =
-          pair(e + 2 < E ? __ldcs(row + e + 2) : -INFINITY, e + 3 < E ? __ldcs(row + e + 3) : -INFINITY);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV / 2; ++i) {
+      const int e = 2 * i * LPR + l;
+      v[i] = pair(e < E ? __ldcs(row + e) : -INFINITY,
+                  e + LPR < E ? __ldcs(row + e + LPR) : -INFINITY);
     }
   }
 }
@@ -279,12 +285,12 @@ struct BalanceWhole {
   float* prob_mean;
 };
 
-template <int LPR, int NV>
-__global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_balance_rows(
+template <int LPR, int NV, bool VEC>
+__global__ void __launch_bounds__(256, RowCfg<LPR, NV, VEC>::kBlocks) k_balance_rows(
     const float* __restrict__ logits, const int* __restrict__ idx,
     const uint8_t* __restrict__ mask, const int* __restrict__ off, int S, int T, int E, int k,
-    int C, int vec, BalancePart part, int* err, const BalanceWhole whole) {
-  using R = RowCfg<LPR, NV>;
+    int C, BalancePart part, int* err, const BalanceWhole whole) {
+  using R = RowCfg<LPR, NV, VEC>;
   extern __shared__ float sm[];
   float* red = sm;                                        // [8][kCols]
   int* hist = reinterpret_cast<int*>(sm + 8 * R::kCols);  // [E]
@@ -328,7 +334,7 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_balance_rows(
         const int r = r0 + u * R::kGroups + g;
         q.in[u] = r < end;
         if (r < end) {
-          load_row<LPR, NV>(logits + (unsigned)(r * E), E, l, vec, q.v[u]);
+          load_row<LPR, NV, VEC>(logits + (unsigned)(r * E), E, l, q.v[u]);
           if (l < k) q.id[u] = __ldg(idx + (unsigned)(r * k + l));
           if (mask) q.in[u] = mask[r] != 0;
         }
@@ -388,10 +394,10 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_balance_rows(
     }
     if (g == 0) {
 #pragma unroll
-      for (int c = 0; c < NV / 4; ++c) {
-        const float2 p0 = unpair(acc[2 * c]), p1 = unpair(acc[2 * c + 1]);
-        *reinterpret_cast<float4*>(red + warp * R::kCols + c * 4 * LPR + 4 * l) =
-            make_float4(p0.x, p0.y, p1.x, p1.y);
+      for (int i = 0; i < NV / 2; ++i) {
+        const float2 q = unpair(acc[i]);
+        red[warp * R::kCols + col_of<LPR, VEC>(l, 2 * i)] = q.x;
+        red[warp * R::kCols + col_of<LPR, VEC>(l, 2 * i + 1)] = q.y;
       }
     }
     if (lane == 0) zred[warp] = zacc, nred[warp] = nacc;
@@ -566,14 +572,14 @@ struct GateArgs {
   const float* dloss;
   float* dlogits;
   float balance_coef, z_coef;
-  int S, T, E, k, rows_per_warp, vec;
+  int S, T, E, k, rows_per_warp;
   int* err;
 };
 
-template <int LPR, int NV>
-__global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_gate_bwd(const GateArgs a) {
-  using R = RowCfg<LPR, NV>;
-  constexpr int RU = NV == 4 ? 2 : 1, kStep = R::kGroups * RU;
+template <int LPR, int NV, bool VEC>
+__global__ void __launch_bounds__(256, RowCfg<LPR, NV, VEC>::kBlocks) k_gate_bwd(const GateArgs a) {
+  using R = RowCfg<LPR, NV, VEC>;
+  constexpr int RU = LPR == 32 && NV == 4 ? 2 : 1, kStep = R::kGroups * RU;
   extern __shared__ float sm[];
   pdl_trigger();
   pdl_wait();
@@ -618,7 +624,7 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_gate_bwd(cons
       q.w[u] = q.dw[u] = 0.f;
       if (t < last) {
         if (aux) {
-          load_row<LPR, NV>(a.logits + (unsigned)(t * a.E), a.E, l, a.vec, q.v[u]);
+          load_row<LPR, NV, VEC>(a.logits + (unsigned)(t * a.E), a.E, l, q.v[u]);
           if (a.mask) q.in[u] = a.mask[t] != 0;
         }
         if (a.dw && l < a.k) {
@@ -649,9 +655,9 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_gate_bwd(cons
             const int* c = a.counts + (size_t)seq * a.E;
 #pragma unroll
             for (int i = 0; i < NV / 2; ++i) {
-              const int e = col_of<LPR, NV>(l, 2 * i);
+              const int e = col_of<LPR, VEC>(l, 2 * i), e1 = col_of<LPR, VEC>(l, 2 * i + 1);
               f[i] = pair(e < a.E ? per * (float)__ldg(c + e) : 0.f,
-                          e + 1 < a.E ? per * (float)__ldg(c + e + 1) : 0.f);
+                          e1 < a.E ? per * (float)__ldg(c + e1) : 0.f);
             }
           }
         }
@@ -710,13 +716,22 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_gate_bwd(cons
             __syncwarp();
           }
         }
+        if constexpr (VEC) {
 #pragma unroll
-        for (int c = 0; c < NV / 4; ++c) {
-          float4* at = reinterpret_cast<float4*>(grow + c * 4 * LPR + 4 * l);
-          const float4 more = *at;
-          q.v[u][2 * c] = add2(q.v[u][2 * c], pair(more.x, more.y));
-          q.v[u][2 * c + 1] = add2(q.v[u][2 * c + 1], pair(more.z, more.w));
-          if (LPR < 32) *at = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int c = 0; c < NV / 4; ++c) {
+            float4* at = reinterpret_cast<float4*>(grow + c * 4 * LPR + 4 * l);
+            const float4 more = *at;
+            q.v[u][2 * c] = add2(q.v[u][2 * c], pair(more.x, more.y));
+            q.v[u][2 * c + 1] = add2(q.v[u][2 * c + 1], pair(more.z, more.w));
+            if (LPR < 32) *at = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NV / 2; ++i) {
+            float* at = grow + 2 * i * LPR + l;
+            q.v[u][i] = add2(q.v[u][i], pair(at[0], at[LPR]));
+            if (LPR < 32) at[0] = at[LPR] = 0.f;
+          }
         }
         __syncwarp();
         if (LPR == 32) {  // k <= 32: one slot a lane
@@ -726,18 +741,21 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_gate_bwd(cons
       }
       if (in) {
         float* out = a.dlogits + (unsigned)(t * a.E);
+        if constexpr (VEC) {
 #pragma unroll
-        for (int c = 0; c < NV / 4; ++c) {
-          const int e = c * 4 * LPR + 4 * l;
-          const float2 o0 = unpair(q.v[u][2 * c]), o1 = unpair(q.v[u][2 * c + 1]);
-          if (a.vec) {
+          for (int c = 0; c < NV / 4; ++c) {
+            const int e = c * 4 * LPR + 4 * l;
+            const float2 o0 = unpair(q.v[u][2 * c]), o1 = unpair(q.v[u][2 * c + 1]);
             if (e < a.E)
               __stcs(reinterpret_cast<float4*>(out + e), make_float4(o0.x, o0.y, o1.x, o1.y));
-          } else {
-            if (e < a.E) __stcs(out + e, o0.x);
-            if (e + 1 < a.E) __stcs(out + e + 1, o0.y);
-            if (e + 2 < a.E) __stcs(out + e + 2, o1.x);
-            if (e + 3 < a.E) __stcs(out + e + 3, o1.y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < NV / 2; ++i) {
+            const int e = 2 * i * LPR + l;
+            const float2 o = unpair(q.v[u][i]);
+            if (e < a.E) __stcs(out + e, o.x);
+            if (e + LPR < a.E) __stcs(out + e + LPR, o.y);
           }
         }
       }
@@ -764,10 +782,11 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV>::kBlocks) k_gate_bwd(cons
 
 // ============================================================== combine backward
 // dw[t,j] = sum_c dy[t,c] z[row_of[t,j],c]; dz[row_of[t,j],c] = w[t,j] dy[t,c].
-// WPR warps per (token, slot): the slots of a token are neighbours, so dy's
-// row comes from L1 for all but the first of them.  A row index outside
-// [0, T*k) gives dw = 0 and writes nothing.
-template <int WPR, bool DW, bool DZ>
+// G lanes per (token, slot): 8 or 16 for rows of 64 or 128 columns, else a warp, or
+// the block's eight warps (G = 256) when there are few rows.  The slots of a token
+// are neighbours, so dy's row comes from L1 for all but the first of them.  A row
+// index outside [0, T*k) gives dw = 0 and writes nothing.
+template <int G, bool DW, bool DZ>
 __global__ void __launch_bounds__(256) k_combine_bwd(
     const __nv_bfloat16* __restrict__ dy, const __nv_bfloat16* __restrict__ z,
     const int* __restrict__ row_of, const float* __restrict__ w, long long P, int d, int k,
@@ -776,7 +795,7 @@ __global__ void __launch_bounds__(256) k_combine_bwd(
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long p = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
+  const long long p = (long long)blockIdx.x * (256 / G) + threadIdx.x / G;
   float acc = 0.f;
   if (p < P) {
     const long long r = __ldg(row_of + p);
@@ -786,12 +805,12 @@ __global__ void __launch_bounds__(256) k_combine_bwd(
       const uint4* zr = reinterpret_cast<const uint4*>(z + (size_t)r * d);
       uint4* gr = reinterpret_cast<uint4*>(dz + (size_t)r * d);
       const int nv = d / 8;
-      constexpr int U = 4, kStep = 32 * WPR;
-      for (int c0 = (warp % WPR) * 32 + lane; c0 < nv; c0 += U * kStep) {
+      constexpr int U = G < 32 ? 1 : 4;
+      for (int c0 = threadIdx.x % G; c0 < nv; c0 += U * G) {
         uint4 yv[U], zv[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int c = c0 + u * kStep;
+          const int c = c0 + u * G;
           yv[u] = zv[u] = make_uint4(0, 0, 0, 0);
           if (c < nv) {
             yv[u] = __ldg(yr + c);
@@ -800,7 +819,7 @@ __global__ void __launch_bounds__(256) k_combine_bwd(
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int c = c0 + u * kStep;
+          const int c = c0 + u * G;
           const __nv_bfloat162* y2 = reinterpret_cast<const __nv_bfloat162*>(&yv[u]);
           const __nv_bfloat162* z2 = reinterpret_cast<const __nv_bfloat162*>(&zv[u]);
           uint4 o;
@@ -821,10 +840,11 @@ __global__ void __launch_bounds__(256) k_combine_bwd(
     }
   }
   if (!DW) return;
+  constexpr int kLanes = G < 32 ? G : 32;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  if (WPR == 1) {
-    if (lane == 0 && p < P) dw[p] = acc;
+  for (int o = kLanes / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (G <= 32) {
+    if (lane % kLanes == 0 && p < P) dw[p] = acc;
     return;
   }
   if (lane == 0) red[warp] = acc;
@@ -838,17 +858,21 @@ __global__ void __launch_bounds__(256) k_combine_bwd(
 }
 
 // fn(RowCfg) for the layout that holds E experts.
+template <bool VEC, class F>
+cudaError_t with_columns(int E, F&& fn) {
+  if (E <= 4) return fn(RowCfg<1, 4, VEC>{});
+  if (E <= 8) return fn(RowCfg<2, 4, VEC>{});
+  if (E <= 16) return fn(RowCfg<4, 4, VEC>{});
+  if (E <= 32) return fn(RowCfg<8, 4, VEC>{});
+  if (E <= 64) return fn(RowCfg<16, 4, VEC>{});
+  if (E <= 128) return fn(RowCfg<32, 4, VEC>{});
+  if (E <= 256) return fn(RowCfg<32, 8, VEC>{});
+  if (E <= 512) return fn(RowCfg<32, 16, VEC>{});
+  return fn(RowCfg<32, 32, VEC>{});
+}
 template <class F>
-cudaError_t with_rows(int E, F&& fn) {
-  if (E <= 4) return fn(RowCfg<1, 4>{});
-  if (E <= 8) return fn(RowCfg<2, 4>{});
-  if (E <= 16) return fn(RowCfg<4, 4>{});
-  if (E <= 32) return fn(RowCfg<8, 4>{});
-  if (E <= 64) return fn(RowCfg<16, 4>{});
-  if (E <= 128) return fn(RowCfg<32, 4>{});
-  if (E <= 256) return fn(RowCfg<32, 8>{});
-  if (E <= 512) return fn(RowCfg<32, 16>{});
-  return fn(RowCfg<32, 32>{});
+cudaError_t with_rows(int E, bool vec, F&& fn) {
+  return vec ? with_columns<true>(E, fn) : with_columns<false>(E, fn);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -862,15 +886,15 @@ cudaError_t launch_balance_loss(const float* logits, const int* idx, const uint8
   BalancePart part{reinterpret_cast<float*>(ws + L.prob), reinterpret_cast<int*>(ws + L.count),
                    reinterpret_cast<float*>(ws + L.z), reinterpret_cast<int*>(ws + L.n)};
   int* err = reinterpret_cast<int*>(ws);
-  const int vec = s.E % 4 == 0 && aligned16(logits);
+  const bool vec = s.E % 4 == 0 && aligned16(logits);
   const int C = L.chunk, nblk = (s.T + C - 1) / C;
   const bool one = nblk == 1 && !off;
   const BalanceWhole whole{balance_coef, z_coef, one ? loss : nullptr, counts, tokens, prob_mean};
-  cudaError_t e = with_rows(s.E, [&](auto cfg) {
+  cudaError_t e = with_rows(s.E, vec, [&](auto cfg) {
     using R = decltype(cfg);
     const size_t smem = sizeof(float) * 8 * R::kCols + sizeof(int) * s.E;
-    return launch_kernel(k_balance_rows<R::kLpr, R::kNv>, dim3(nblk), dim3(256), smem, st, 1,
-                         logits, idx, mask, off, S, s.T, s.E, s.k, C, vec, part, err, whole);
+    return launch_kernel(k_balance_rows<R::kLpr, R::kNv, R::kVec>, dim3(nblk), dim3(256), smem,
+                         st, 1, logits, idx, mask, off, S, s.T, s.E, s.k, C, part, err, whole);
   });
   if (e != cudaSuccess || one) return e;
   const auto finish = [&](auto kern, int warps) {
@@ -889,10 +913,10 @@ cudaError_t launch_gate_bwd(const float* logits, const int* idx, const float* w,
                             const int* tokens, const moe_shape& s, float balance_coef,
                             float z_coef, const float* dloss, float* dlogits, int* err, int sms,
                             cudaStream_t st) {
-  const int vec = s.E % 4 == 0 && (!counts || aligned16(logits)) && aligned16(dlogits);
+  const bool vec = s.E % 4 == 0 && (!counts || aligned16(logits)) && aligned16(dlogits);
   GateArgs a{logits, idx, w, dw, mask, off, counts, tokens, dloss, dlogits, balance_coef, z_coef,
-             S, s.T, s.E, s.k, 1, vec, err};
-  return with_rows(s.E, [&](auto cfg) {
+             S, s.T, s.E, s.k, 1, err};
+  return with_rows(s.E, vec, [&](auto cfg) {
     using R = decltype(cfg);
     // One run of whole groups for each warp that the SMs hold (two or four rounds of
     // shorter runs: 3% and 10% slower at 131072 x 256).
@@ -902,7 +926,7 @@ cudaError_t launch_gate_bwd(const float* logits, const int* idx, const float* w,
     a.rows_per_warp = (int)rows;
     const long long nw = (s.T + rows - 1) / rows;
     const size_t smem = sizeof(float) * 8 * R::kGroups * R::kCols;
-    return launch_kernel(k_gate_bwd<R::kLpr, R::kNv>, dim3((unsigned)((nw + 7) / 8)), dim3(256),
+    return launch_kernel(k_gate_bwd<R::kLpr, R::kNv, R::kVec>, dim3((unsigned)((nw + 7) / 8)), dim3(256),
                          smem, st, 1, a);
   });
 }
@@ -911,18 +935,25 @@ cudaError_t launch_combine_bwd(const __nv_bfloat16* dy, const __nv_bfloat16* z, 
                                const float* w, const moe_shape& s, float* dw, __nv_bfloat16* dz,
                                int sms, cudaStream_t st) {
   const long long P = (long long)s.T * s.k;
-  // Few rows: eight warps a row, so that more loads are in flight.
-  const bool wide = P < 16LL * sms;
-  const unsigned blocks = (unsigned)(wide ? P : (P + 7) / 8);
+  // Few rows of some length: eight warps a row, so that more loads are in flight.
+  const bool wide = P < 16LL * sms && s.d > 256;
+  const int lanes = wide ? 256 : s.d == 64 ? 8 : s.d == 128 ? 16 : 32;
+  const unsigned blocks = (unsigned)((P * lanes + 255) / 256);
   auto go = [&](auto kern) {
     return launch_kernel(kern, dim3(blocks), dim3(256), 0, st, 1, dy, z, row_of, w, P, s.d, s.k,
                          dw, dz);
   };
-  if (wide)
-    return dw && dz ? go(k_combine_bwd<8, true, true>)
-                    : dw ? go(k_combine_bwd<8, true, false>) : go(k_combine_bwd<8, false, true>);
-  return dw && dz ? go(k_combine_bwd<1, true, true>)
-                  : dw ? go(k_combine_bwd<1, true, false>) : go(k_combine_bwd<1, false, true>);
+  auto pick = [&](auto g) {
+    constexpr int G = decltype(g)::value;
+    return dw && dz ? go(k_combine_bwd<G, true, true>)
+                    : dw ? go(k_combine_bwd<G, true, false>) : go(k_combine_bwd<G, false, true>);
+  };
+  switch (lanes) {
+    case 8: return pick(std::integral_constant<int, 8>{});
+    case 16: return pick(std::integral_constant<int, 16>{});
+    case 32: return pick(std::integral_constant<int, 32>{});
+    default: return pick(std::integral_constant<int, 256>{});
+  }
 }
 
 }  // namespace moe

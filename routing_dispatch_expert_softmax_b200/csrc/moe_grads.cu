@@ -15,7 +15,8 @@ namespace {
 
 constexpr int kUnit = 2048;       // elements
 constexpr int kPiece = 32;        // most units of a block's run in one round
-constexpr int kGradTable = 256;   // tensors of one launch
+constexpr int kSmallTable = 64;   // tensors of one launch: the small table, or
+constexpr int kGradTable = 768;   // the large one (24 KB of the 32 KB of a launch's parameters)
 constexpr int kGradBlocks = 592;  // blocks of one launch (partial sums), 4 for each SM
 
 struct GradEntry {
@@ -27,13 +28,15 @@ struct GradEntry {
   int out_bf16;
 };
 
+template <int N>
 struct GradTable {
-  GradEntry e[kGradTable];
-  int count;        // entries
   long long units;  // of all entries
+  int count;        // entries
+  GradEntry e[N];
 };
 
-__device__ __forceinline__ const GradEntry& entry_of(const GradTable& t, long long u) {
+template <int N>
+__device__ __forceinline__ const GradEntry& entry_of(const GradTable<N>& t, long long u) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -44,10 +47,12 @@ __device__ __forceinline__ const GradEntry& entry_of(const GradTable& t, long lo
 }
 
 // Rounds of the sequence, and the units [first, last) of this block's run in one.
-__device__ __forceinline__ long long rounds_of(const GradTable& t) {
+template <int N>
+__device__ __forceinline__ long long rounds_of(const GradTable<N>& t) {
   return (t.units + (long long)gridDim.x * kPiece - 1) / ((long long)gridDim.x * kPiece);
 }
-__device__ __forceinline__ void run_of(const GradTable& t, long long round, long long rounds,
+template <int N>
+__device__ __forceinline__ void run_of(const GradTable<N>& t, long long round, long long rounds,
                                        long long& first, long long& last) {
   const long long r0 = t.units * round / rounds, n = t.units * (round + 1) / rounds - r0;
   first = r0 + n * blockIdx.x / gridDim.x;
@@ -147,7 +152,8 @@ __device__ double sum_squares(const T* __restrict__ p, int n) {
 
 // Block partials of this launch go to partial[first ...]; the last block of
 // the list's last launch (done != nullptr) adds up all of them in order.
-__global__ void __launch_bounds__(256) k_grad_sumsq(const __grid_constant__ GradTable t,
+template <int N>
+__global__ void __launch_bounds__(256) k_grad_sumsq(const __grid_constant__ GradTable<N> t,
                                                     double* __restrict__ partial, int first,
                                                     double* __restrict__ sumsq, int last_launch,
                                                     unsigned* __restrict__ ticket) {
@@ -284,7 +290,8 @@ __device__ void scale(const TI* in, TO* out, int n, float c, const char* lo, con
   for (int at = h + nv * N + (int)threadIdx.x; at < n; at += 256) put(out + at, c * widen(in[at]));
 }
 
-__global__ void __launch_bounds__(256) k_grad_scale(const __grid_constant__ GradTable t,
+template <int N>
+__global__ void __launch_bounds__(256) k_grad_scale(const __grid_constant__ GradTable<N> t,
                                                     const double* __restrict__ sumsq,
                                                     float max_norm, float* __restrict__ norm) {
   pdl_trigger();
@@ -319,15 +326,15 @@ __global__ void __launch_bounds__(256) k_grad_scale(const __grid_constant__ Grad
   }
 }
 
-// Calls fn(table, grid, launch index, is the last) for each 256 tensors.
-template <class F>
+// Calls fn(table, grid, launch index, is the last) for each N tensors.
+template <int N, class F>
 cudaError_t for_tables(const moe_grad* g, int n, F&& fn) {
-  const int launches = std::max(1, (n + kGradTable - 1) / kGradTable);
+  const int launches = std::max(1, (n + N - 1) / N);
   for (int q = 0; q < launches; ++q) {
-    GradTable t;
+    GradTable<N> t;
     t.count = 0;
     t.units = 0;
-    for (int i = q * kGradTable; i < std::min(n, (q + 1) * kGradTable); ++i) {
+    for (int i = q * N; i < std::min(n, (q + 1) * N); ++i) {
       if (g[i].n == 0) continue;
       t.e[t.count++] = GradEntry{g[i].data, g[i].out, g[i].n, t.units,
                                  g[i].dtype == MOE_GRAD_BF16, g[i].out_dtype == MOE_GRAD_BF16};
@@ -338,6 +345,28 @@ cudaError_t for_tables(const moe_grad* g, int n, F&& fn) {
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+template <int N>
+cudaError_t sumsq(const moe_grad* g, int n, double* out, void* ws, cudaStream_t st) {
+  double* partial = reinterpret_cast<double*>(static_cast<char*>(ws) + 512);
+  unsigned* ticket = static_cast<unsigned*>(ws) + kGradTicket;
+  int first = 0;
+  return for_tables<N>(g, n, [&](const GradTable<N>& t, int grid, int, bool last) {
+    const cudaError_t e = launch_kernel(k_grad_sumsq<N>, dim3(grid), dim3(256), 0, st, 1, t,
+                                        partial, first, out, (int)last, ticket);
+    first += grid;
+    return e;
+  });
+}
+
+template <int N>
+cudaError_t scale_all(const moe_grad* g, int n, const double* sumsq, float max_norm, float* norm,
+                      cudaStream_t st) {
+  return for_tables<N>(g, n, [&](const GradTable<N>& t, int grid, int q, bool) {
+    return launch_kernel(k_grad_scale<N>, dim3(grid), dim3(256), 0, st, 1, t, sumsq, max_norm,
+                         q == 0 ? norm : nullptr);
+  });
 }
 
 }  // namespace
@@ -351,25 +380,15 @@ double* grads_ws_sumsq(void* ws) {
   return reinterpret_cast<double*>(static_cast<char*>(ws) + 256);
 }
 
-cudaError_t launch_grad_sumsq(const moe_grad* g, int n, double* sumsq, void* ws,
-                              cudaStream_t st) {
-  double* partial = reinterpret_cast<double*>(static_cast<char*>(ws) + 512);
-  unsigned* ticket = static_cast<unsigned*>(ws) + kGradTicket;
-  int first = 0;
-  return for_tables(g, n, [&](const GradTable& t, int grid, int, bool last) {
-    const cudaError_t e = launch_kernel(k_grad_sumsq, dim3(grid), dim3(256), 0, st, 1,
-                                        t, partial, first, sumsq, (int)last, ticket);
-    first += grid;
-    return e;
-  });
+cudaError_t launch_grad_sumsq(const moe_grad* g, int n, double* out, void* ws, cudaStream_t st) {
+  return n <= kSmallTable ? sumsq<kSmallTable>(g, n, out, ws, st)
+                          : sumsq<kGradTable>(g, n, out, ws, st);
 }
 
 cudaError_t launch_grad_scale(const moe_grad* g, int n, const double* sumsq, float max_norm,
                               float* norm, cudaStream_t st) {
-  return for_tables(g, n, [&](const GradTable& t, int grid, int q, bool) {
-    return launch_kernel(k_grad_scale, dim3(grid), dim3(256), 0, st, 1, t, sumsq,
-                         max_norm, q == 0 ? norm : nullptr);
-  });
+  return n <= kSmallTable ? scale_all<kSmallTable>(g, n, sumsq, max_norm, norm, st)
+                          : scale_all<kGradTable>(g, n, sumsq, max_norm, norm, st);
 }
 
 }  // namespace moe

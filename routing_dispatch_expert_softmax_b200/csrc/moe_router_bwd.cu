@@ -614,31 +614,47 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
   if (warp == 1) tmem_dealloc(tmem_base, 512);
 }
 
-// dw = the ranges' tiles added in order (blocks [0, dw_blocks)); db = the
+// dw = the partials added in a fixed order (blocks [0, dw_blocks)): a block has 1024 / G
+// values, which G groups of its threads sum over every G-th partial each.  db = the
 // column sums of the dL blocks added in fp64 (8 experts a block, 32 threads each).
-__global__ void __launch_bounds__(256) k_router_sum(const float* __restrict__ part, int ranges,
+template <int G>
+__global__ void __launch_bounds__(256) k_router_sum(const float* __restrict__ part, int partials,
                                                     long long n, float* __restrict__ dw,
                                                     int dw_blocks, const float* __restrict__ sums,
                                                     int sum_rows, int E, float* __restrict__ db) {
   __shared__ double red[32][8];
+  __shared__ float4 meet[G > 1 ? 256 : 1];
   pdl_trigger();
   pdl_wait();
   if ((int)blockIdx.x < dw_blocks) {
     // n is a multiple of 64 (d is); dw itself may be aligned to 4 bytes only
-    const bool vec = (reinterpret_cast<uintptr_t>(dw) & 15) == 0;
-    const float4* p4 = reinterpret_cast<const float4*>(part);
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n / 4; i += dw_blocks * 256LL) {
-      float4 s = __ldcs(p4 + i);
+    constexpr int kSpan = 256 / G;
+    const int c = threadIdx.x % kSpan, g = threadIdx.x / kSpan;
+    const long long i = (long long)blockIdx.x * kSpan + c, n4 = n / 4;
+    const float4* p4 = reinterpret_cast<const float4*>(part) + i;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < n4) {
 #pragma unroll 8
-      for (int p = 1; p < ranges; ++p) {
-        const float4 v = __ldcs(p4 + p * (n / 4) + i);
+      for (int p = g; p < partials; p += G) {
+        const float4 v = __ldcs(p4 + p * n4);
         s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
       }
-      if (vec) {
-        reinterpret_cast<float4*>(dw)[i] = s;
-      } else {
-        dw[4 * i] = s.x, dw[4 * i + 1] = s.y, dw[4 * i + 2] = s.z, dw[4 * i + 3] = s.w;
+    }
+    if (G > 1) {
+      meet[threadIdx.x] = s;
+      __syncthreads();
+      if (g > 0) return;
+#pragma unroll
+      for (int k = 1; k < G; ++k) {
+        const float4 v = meet[k * kSpan + c];
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
       }
+    }
+    if (i >= n4) return;
+    if ((reinterpret_cast<uintptr_t>(dw) & 15) == 0) {
+      reinterpret_cast<float4*>(dw)[i] = s;
+    } else {
+      dw[4 * i] = s.x, dw[4 * i + 1] = s.y, dw[4 * i + 2] = s.z, dw[4 * i + 3] = s.w;
     }
     return;
   }
@@ -766,11 +782,16 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
     if (e != cudaSuccess) return e;
   }
   const long long n = (long long)d * E;
-  const int dw_blocks = dw && !direct ? (int)std::min<long long>((n / 4 + 255) / 256, 8LL * sms) : 0;
+  const int partials = ranges * pl.parts, groups = partials >= 16 ? 8 : 1;
+  const int span = 1024 / groups;  // values of one block
+  const int dw_blocks = dw && !direct ? (int)((n + span - 1) / span) : 0;
   const int db_blocks = db && sum_rows > 1 ? (E + 7) / 8 : 0;
   if (dw_blocks + db_blocks == 0) return e;
-  return launch_kernel(k_router_sum, dim3(dw_blocks + db_blocks), dim3(256), 0, st, 1, part,
-                       ranges * pl.parts, n, dw, dw_blocks, sums, sum_rows, E, db);
+  const auto sum = [&](auto kern) {
+    return launch_kernel(kern, dim3(dw_blocks + db_blocks), dim3(256), 0, st, 1, part, partials, n,
+                         dw, dw_blocks, sums, sum_rows, E, db);
+  };
+  return groups == 8 ? sum(k_router_sum<8>) : sum(k_router_sum<1>);
 }
 
 }  // namespace moe

@@ -557,7 +557,7 @@ def test_clip_into_a_flat_buffer(max_norm, types):
         assert torch.isnan(flat[-1])
 
 
-@pytest.mark.parametrize("n", [1, 255, 256, 257, 700])
+@pytest.mark.parametrize("n", [1, 64, 65, 767, 768, 769, 1600])
 def test_clip_many_tensors(n):
     r = np.random.default_rng(n)
     check_clip([int(v) for v in r.integers(0, 300, n)], [H if i % 3 else F for i in range(n)], 1.0)
