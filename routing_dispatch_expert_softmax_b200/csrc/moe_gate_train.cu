@@ -17,19 +17,24 @@ namespace {
 // A group of LPR lanes owns one row of E fp32 logits, NV values a lane: in chunks
 // of 4, chunk c of lane l the columns c * 4 * LPR + 4 l + (0..3), so that a group's
 // 16-byte loads are contiguous; or, where rows are not 16-byte aligned, value i the
-// column i * LPR + l, so that its 4-byte loads are (VEC = false).  Up to 128 experts a lane holds
-// 4 values and a warp 32 / LPR rows at once; above, a whole warp takes one row.
-// Each group works on kRows rows together (their shuffle chains overlap) and, up
-// to 512 experts, has the next ones' loads in flight meanwhile.
+// column i * LPR + l, so that its 4-byte loads are (VEC = false).
+//
+// These kernels are bound by the instructions of a row that do not shrink with it
+// (reductions, the k slots), so a lane holds 8 values up to 256 experts and a warp
+// takes 32 / LPR rows at once: with 4 values (two rows of 64 experts a warp in place
+// of four, one of 128 in place of two) the gate's gradient of 131072 rows takes 29
+// and 49 us in place of 21 and 36.  Above 256 experts a warp has one row.  The next
+// rows' loads are in flight meanwhile, up to 512 experts.
 template <int LPR, int NV, bool VEC>
 struct RowCfg {
   static constexpr int kLpr = LPR, kNv = NV;
   static constexpr bool kVec = VEC;
   static constexpr int kGroups = 32 / LPR;  // rows of a warp at once
   static constexpr int kCols = LPR * NV;    // columns a group can hold
-  static constexpr int kRows = NV == 4 ? 2 : 1;
   static constexpr bool kAhead = NV <= 16;
-  static constexpr int kBlocks = NV <= 8 ? 4 : NV <= 16 ? 3 : 2;  // blocks of an SM
+  // blocks of an SM: of the balance loss, of the gate's gradient
+  static constexpr int kBlocks = NV <= 8 ? 4 : NV <= 16 ? 3 : 2;
+  static constexpr int kGateBlocks = NV > 8 ? 2 : LPR == 1 || LPR == 32 ? 4 : 3;
 };
 
 template <int LPR, bool VEC>
@@ -137,75 +142,45 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Each row's values become exp(v - max); gives the lane's sum of them (rows_sum and
-// sum3 add the group's up) and the row's maximum.
-// live: some value is not -inf (a NaN counts: it has to show in the result).
-// A row without a live value gives exp values of 0 and a sum of 0.
+// A row's values become exp(v - max); returns the lane's sum of them and gives the
+// row's maximum.  live: some value is not -inf (a NaN counts: it has to show in the
+// result).  A row without a live value gives exp values of 0 and a sum of 0.
 // exp is ex2.approx of the difference times log2 e: with a difference of size D
 // off by at most (2.3 D + 4) 2^-24 of the value, and values below 2^-126 are 0.
 // These kernels are bound by their instructions, of which expf takes four times as many.
-template <int LPR, int NV, int RU>
-__device__ __forceinline__ void rows_exp(f32x2 (&v)[RU][NV / 2], float (&top)[RU],
-                                         float (&sum)[RU], bool (&live)[RU]) {
+template <int LPR, int NV>
+__device__ __forceinline__ float row_exp(f32x2 (&v)[NV / 2], float& top, bool& live) {
+  float m = -INFINITY;
 #pragma unroll
-  for (int u = 0; u < RU; ++u) {
-    float m = -INFINITY;
+  for (int i = 0; i < NV / 2; ++i) {
+    const float2 q = unpair(v[i]);
+    m = max3(m, q.x, q.y);
+  }
+  top = group_max<LPR>(m);
+  live = top != -INFINITY;
+  if (!__all_sync(0xffffffffu, live)) {  // nothing but -inf, and perhaps NaN
+    bool nan = false;
 #pragma unroll
     for (int i = 0; i < NV / 2; ++i) {
-      const float2 q = unpair(v[u][i]);
-      m = max3(m, q.x, q.y);
+      const float2 q = unpair(v[i]);
+      nan |= q.x != q.x || q.y != q.y;
     }
-    top[u] = m;
+    const unsigned votes = __ballot_sync(0xffffffffu, nan);
+    const int g0 = (threadIdx.x & 31) / LPR * LPR;
+    const unsigned mine = LPR == 32 ? votes : (votes >> g0) & ((1u << (LPR & 31)) - 1u);
+    // with 0 in the maximum's place the -inf values keep giving 0
+    if (!live) top = 0.f, live = mine != 0;
   }
+  const f32x2 down = pair(-top, -top), log2e = pair(kLog2e, kLog2e);
+  f32x2 t = 0;
 #pragma unroll
-  for (int u = 0; u < RU; ++u) top[u] = group_max<LPR>(top[u]);
-#pragma unroll
-  for (int u = 0; u < RU; ++u) {
-    live[u] = top[u] != -INFINITY;
-    if (!__all_sync(0xffffffffu, live[u])) {  // nothing but -inf, and perhaps NaN
-      bool nan = false;
-#pragma unroll
-      for (int i = 0; i < NV / 2; ++i) {
-        const float2 q = unpair(v[u][i]);
-        nan |= q.x != q.x || q.y != q.y;
-      }
-      const unsigned votes = __ballot_sync(0xffffffffu, nan);
-      const int g0 = (threadIdx.x & 31) / LPR * LPR;
-      const unsigned mine = LPR == 32 ? votes : (votes >> g0) & ((1u << (LPR & 31)) - 1u);
-      // with 0 in the maximum's place the -inf values keep giving 0
-      if (!live[u]) top[u] = 0.f, live[u] = mine != 0;
-    }
-    const f32x2 down = pair(-top[u], -top[u]), log2e = pair(kLog2e, kLog2e);
-    f32x2 t = 0;
-#pragma unroll
-    for (int i = 0; i < NV / 2; ++i) {
-      const float2 q = unpair(mul2(add2(v[u][i], down), log2e));
-      v[u][i] = pair(exp2_fast(q.x), exp2_fast(q.y));
-      t = i ? add2(t, v[u][i]) : v[u][i];
-    }
-    const float2 q = unpair(t);
-    sum[u] = q.x + q.y;
+  for (int i = 0; i < NV / 2; ++i) {
+    const float2 q = unpair(mul2(add2(v[i], down), log2e));
+    v[i] = pair(exp2_fast(q.x), exp2_fast(q.y));
+    t = i ? add2(t, v[i]) : v[i];
   }
-}
-
-// Each row's sum over its group of lanes.
-template <int LPR, int RU>
-__device__ __forceinline__ void rows_sum(float (&sum)[RU]) {
-  if constexpr (LPR == 32 && RU == 2) {
-    // both rows in one chain: half a warp goes on with each
-    const bool hi = (threadIdx.x & 16) != 0;
-    float t = hi ? sum[1] : sum[0];
-    t += __shfl_xor_sync(0xffffffffu, hi ? sum[0] : sum[1], 16);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-    sum[0] = __shfl_sync(0xffffffffu, t, 0);
-    sum[1] = __shfl_sync(0xffffffffu, t, 16);
-  } else {
-#pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1)
-#pragma unroll
-      for (int u = 0; u < RU; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
-  }
+  const float2 q = unpair(t);
+  return q.x + q.y;
 }
 
 // Three sums over each group of lanes; a whole warp does them in one chain, a
@@ -321,66 +296,56 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV, VEC>::kBlocks) k_balance_
     for (int i = 0; i < NV / 2; ++i) acc[i] = 0;
     float zacc = 0.f;
     int nacc = 0;
-    constexpr int RU = R::kRows, kStep = 8 * R::kGroups * RU;
-    struct Rows {
-      f32x2 v[RU][NV / 2];
-      int id[RU];  // the lane's first selection
-      bool in[RU];
+    constexpr int kStep = 8 * R::kGroups;
+    struct Row {
+      f32x2 v[NV / 2];
+      int id;  // the lane's first selection
+      bool in;
     };
-    // rows r0 + u * kGroups + g
-    auto load = [&](Rows& q, int r0) {
-#pragma unroll
-      for (int u = 0; u < RU; ++u) {
-        const int r = r0 + u * R::kGroups + g;
-        q.in[u] = r < end;
-        if (r < end) {
-          load_row<LPR, NV, VEC>(logits + (unsigned)(r * E), E, l, q.v[u]);
-          if (l < k) q.id[u] = __ldg(idx + (unsigned)(r * k + l));
-          if (mask) q.in[u] = mask[r] != 0;
-        }
+    auto load = [&](Row& q, int r) {
+      q.in = r < end;
+      if (r < end) {
+        load_row<LPR, NV, VEC>(logits + (unsigned)(r * E), E, l, q.v);
+        if (l < k) q.id = __ldg(idx + (unsigned)(r * k + l));
+        if (mask) q.in = mask[r] != 0;
       }
     };
     auto count = [&](int e) {
       if ((unsigned)e < (unsigned)E) atomicAdd(&hist[e], 1);
       else bad_id = true;
     };
-    auto add_rows = [&](Rows& q, int r0) {
-      float top[RU], sum[RU];
-      bool live[RU];
-      rows_exp<LPR, NV, RU>(q.v, top, sum, live);
-      rows_sum<LPR, RU>(sum);
+    auto add_row = [&](Row& q, int r) {
+      float top;
+      bool live;
+      const float sum = group_sum<LPR>(row_exp<LPR, NV>(q.v, top, live));
+      if (!(q.in && live)) return;
+      const float inv = rcp_fast(sum);
+      const f32x2 inv2 = pair(inv, inv);
 #pragma unroll
-      for (int u = 0; u < RU; ++u) {
-        if (!(q.in[u] && live[u])) continue;
-        const float inv = rcp_fast(sum[u]);
-        const f32x2 inv2 = pair(inv, inv);
-#pragma unroll
-        for (int i = 0; i < NV / 2; ++i) acc[i] = fma2(q.v[u][i], inv2, acc[i]);
-        const float lse = top[u] + log_fast(sum[u]);  // every lane of the group the same
-        zacc = fmaf(lse, lse, zacc);
-        ++nacc;
-        if (l < k) count(q.id[u]);
-        if (LPR < 32) {
-          const int r = r0 + u * R::kGroups + g;
-          for (int j = l + LPR; j < k; j += LPR) count(__ldg(idx + (size_t)r * k + j));
-        }
-      }
+      for (int i = 0; i < NV / 2; ++i) acc[i] = fma2(q.v[i], inv2, acc[i]);
+      const float lse = top + log_fast(sum);  // every lane of the group the same
+      zacc = fmaf(lse, lse, zacc);
+      ++nacc;
+      if (l < k) count(q.id);
+      if (LPR < 32)
+        for (int j = l + LPR; j < k; j += LPR) count(__ldg(idx + (unsigned)(r * k + j)));
     };
-    const int first = t + warp * R::kGroups * RU;
-    Rows even = {}, odd = {};
+    // the group's rows are g, g + kStep, ...; a warp's groups stay together
+    const int first = t + warp * R::kGroups;
+    Row even = {}, odd = {};
     if constexpr (R::kAhead) {
-      if (first < end) load(even, first);
+      if (first < end) load(even, first + g);
       for (int r0 = first; r0 < end; r0 += 2 * kStep) {
-        load(odd, r0 + kStep);  // past the end: nothing is read, nothing counts
-        add_rows(even, r0);
+        load(odd, r0 + kStep + g);  // past the end: nothing is read, nothing counts
+        add_row(even, r0 + g);
         if (r0 + kStep >= end) break;
-        load(even, r0 + 2 * kStep);
-        add_rows(odd, r0 + kStep);
+        load(even, r0 + 2 * kStep + g);
+        add_row(odd, r0 + kStep + g);
       }
     } else {
       for (int r0 = first; r0 < end; r0 += kStep) {
-        load(even, r0);
-        add_rows(even, r0);
+        load(even, r0 + g);
+        add_row(even, r0 + g);
       }
     }
     // groups of the warp, then the block's 8 warps
@@ -577,9 +542,9 @@ struct GateArgs {
 };
 
 template <int LPR, int NV, bool VEC>
-__global__ void __launch_bounds__(256, RowCfg<LPR, NV, VEC>::kBlocks) k_gate_bwd(const GateArgs a) {
+__global__ void __launch_bounds__(256, RowCfg<LPR, NV, VEC>::kGateBlocks) k_gate_bwd(const GateArgs a) {
   using R = RowCfg<LPR, NV, VEC>;
-  constexpr int RU = LPR == 32 && NV == 4 ? 2 : 1, kStep = R::kGroups * RU;
+  constexpr int kStep = R::kGroups;
   extern __shared__ float sm[];
   pdl_trigger();
   pdl_wait();
@@ -608,173 +573,158 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV, VEC>::kBlocks) k_gate_bwd
   for (int i = 0; i < NV / 2; ++i) f[i] = 0;
   int seq = -2, seq_end = -1;  // [.., seq_end) is the run whose f is loaded
   bool bad_id = false;
-  struct Rows {
-    f32x2 v[RU][NV / 2];
-    float w[RU], dw[RU];  // the lane's first slot
-    int id[RU];
-    bool in[RU];
+  struct Row {
+    f32x2 v[NV / 2];
+    float w, dw;  // the lane's first slot
+    int id;
+    bool in;
   };
-  // rows r0 + u * kGroups + g: logits and the lane's first slot
-  auto load = [&](Rows& q, int r0) {
-#pragma unroll
-    for (int u = 0; u < RU; ++u) {
-      const int t = r0 + u * R::kGroups + g;
-      q.in[u] = t < last;
-      q.id[u] = -1;
-      q.w[u] = q.dw[u] = 0.f;
-      if (t < last) {
-        if (aux) {
-          load_row<LPR, NV, VEC>(a.logits + (unsigned)(t * a.E), a.E, l, q.v[u]);
-          if (a.mask) q.in[u] = a.mask[t] != 0;
-        }
-        if (a.dw && l < a.k) {
-          const unsigned at = t * a.k + l;
-          q.id[u] = __ldg(a.idx + at);
-          q.w[u] = __ldg(a.w + at);
-          q.dw[u] = __ldg(a.dw + at);
-        }
+  auto load = [&](Row& q, int t) {
+    q.in = t < last;
+    q.id = -1;
+    q.w = q.dw = 0.f;
+    if (t < last) {
+      if (aux) {
+        load_row<LPR, NV, VEC>(a.logits + (unsigned)(t * a.E), a.E, l, q.v);
+        if (a.mask) q.in = a.mask[t] != 0;
+      }
+      if (a.dw && l < a.k) {
+        const unsigned at = t * a.k + l;
+        q.id = __ldg(a.idx + at);
+        q.w = __ldg(a.w + at);
+        q.dw = __ldg(a.dw + at);
       }
     }
   };
-  auto grad_rows = [&](Rows& q, int r0) {
-    float top[RU], sum[RU] = {}, dot[RU] = {}, dotw[RU];
-    bool live[RU] = {};
-    if (aux) rows_exp<LPR, NV, RU>(q.v, top, sum, live);
+  auto grad_row = [&](Row& q, int t) {
+    const bool in = t < last;
+    float top = 0.f, sum = 0.f, dot = 0.f;
+    bool live = false;
+    if (aux) {
+      sum = row_exp<LPR, NV>(q.v, top, live);
+      if (in && t >= seq_end) {
+        seq = a.off ? find_seq(a.off, a.S, t) : 0;
+        const bool real = seq >= 0 && seq < a.S;
+        seq_end = !a.off || seq >= a.S ? a.T : __ldg(a.off + seq + 1);
+        if (real && cf != 0.f) {
+          const int n = max(1, __ldg(a.tokens + seq));
+          const float per =
+              cf * (float)a.E / ((float)live_seqs * (float)a.k * (float)n * (float)n);
+          const int* c = a.counts + (size_t)seq * a.E;
 #pragma unroll
-    for (int u = 0; u < RU; ++u) {
-      const int t = r0 + u * R::kGroups + g;
-      if (aux) {
-        if (t < last && t >= seq_end) {
-          seq = a.off ? find_seq(a.off, a.S, t) : 0;
-          const bool real = seq >= 0 && seq < a.S;
-          seq_end = !a.off || seq >= a.S ? a.T : __ldg(a.off + seq + 1);
-          if (real && cf != 0.f) {
-            const int n = max(1, __ldg(a.tokens + seq));
-            const float per =
-                cf * (float)a.E / ((float)live_seqs * (float)a.k * (float)n * (float)n);
-            const int* c = a.counts + (size_t)seq * a.E;
-#pragma unroll
-            for (int i = 0; i < NV / 2; ++i) {
-              const int e = col_of<LPR, VEC>(l, 2 * i), e1 = col_of<LPR, VEC>(l, 2 * i + 1);
-              f[i] = pair(e < a.E ? per * (float)__ldg(c + e) : 0.f,
-                          e1 < a.E ? per * (float)__ldg(c + e1) : 0.f);
-            }
+          for (int i = 0; i < NV / 2; ++i) {
+            const int e = col_of<LPR, VEC>(l, 2 * i), e1 = col_of<LPR, VEC>(l, 2 * i + 1);
+            f[i] = pair(e < a.E ? per * (float)__ldg(c + e) : 0.f,
+                        e1 < a.E ? per * (float)__ldg(c + e1) : 0.f);
           }
         }
-        live[u] = live[u] && q.in[u] && seq >= 0 && seq < a.S;
-        f32x2 d = mul2(f[0], q.v[u][0]);
-#pragma unroll
-        for (int i = 1; i < NV / 2; ++i) d = fma2(f[i], q.v[u][i], d);
-        const float2 h = unpair(d);
-        dot[u] = h.x + h.y;
       }
-      dotw[u] = q.w[u] * q.dw[u];
-      if (LPR < 32 && a.dw && t < last)
-        for (int j = l + LPR; j < a.k; j += LPR)
-          dotw[u] = fmaf(__ldg(a.w + (unsigned)(t * a.k + j)), __ldg(a.dw + (unsigned)(t * a.k + j)),
-                         dotw[u]);
-      sum3<LPR>(sum[u], dot[u], dotw[u]);
-      if (aux && live[u]) {
-        // v / sum (f + zc lse - dot / sum)
-        const float inv = rcp_fast(sum[u]);
-        const float add =
-            inv * ((zc != 0.f ? zc * (top[u] + log_fast(sum[u])) : 0.f) - dot[u] * inv);
-        const f32x2 inv2 = pair(inv, inv), add2x = pair(add, add);
+      live = live && q.in && seq >= 0 && seq < a.S;
+      f32x2 d = mul2(f[0], q.v[0]);
 #pragma unroll
-        for (int i = 0; i < NV / 2; ++i) q.v[u][i] = mul2(q.v[u][i], fma2(f[i], inv2, add2x));
+      for (int i = 1; i < NV / 2; ++i) d = fma2(f[i], q.v[i], d);
+      const float2 h = unpair(d);
+      dot = h.x + h.y;
+    }
+    float dotw = q.w * q.dw;
+    if (LPR < 32 && a.dw && in)
+      for (int j = l + LPR; j < a.k; j += LPR)
+        dotw = fmaf(__ldg(a.w + (unsigned)(t * a.k + j)), __ldg(a.dw + (unsigned)(t * a.k + j)), dotw);
+    sum3<LPR>(sum, dot, dotw);
+    if (live) {
+      // v / sum (f + zc lse - dot / sum)
+      const float inv = rcp_fast(sum);
+      const float add = inv * ((zc != 0.f ? zc * (top + log_fast(sum)) : 0.f) - dot * inv);
+      const f32x2 inv2 = pair(inv, inv), more = pair(add, add);
+#pragma unroll
+      for (int i = 0; i < NV / 2; ++i) q.v[i] = mul2(q.v[i], fma2(f[i], inv2, more));
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV / 2; ++i) q.v[i] = 0;
+    }
+    if (a.dw) {
+      // A step adds the slots j0 .. j0 + LPR - 1.  Ids are distinct in a token;
+      // should two slots of a step share one, the lower slot goes first.
+      for (int j0 = 0; j0 < a.k; j0 += LPR) {
+        int e = q.id;
+        float wj = q.w, dwj = q.dw;
+        if (LPR < 32 && j0 > 0) {
+          e = -1;
+          if (in && j0 + l < a.k) {
+            const unsigned at = t * a.k + j0 + l;
+            e = __ldg(a.idx + at), wj = __ldg(a.w + at), dwj = __ldg(a.dw + at);
+          }
+        }
+        if (in && j0 + l < a.k && (unsigned)e >= (unsigned)a.E) bad_id = true;
+        const bool has = (unsigned)e < (unsigned)a.E;
+        const float term = wj * (dwj - dotw);
+        const unsigned same = __match_any_sync(0xffffffffu, has ? g * a.E + e : -1 - lane);
+        const int before = __popc(same & ((1u << lane) - 1u));
+        if (has && before == 0) grow[e] = LPR < 32 ? grow[e] + term : term;
+        __syncwarp();
+        for (int turn = 1; __any_sync(0xffffffffu, before >= turn); ++turn) {
+          if (has && before == turn) grow[e] += term;
+          __syncwarp();
+        }
+      }
+      if constexpr (VEC) {
+#pragma unroll
+        for (int c = 0; c < NV / 4; ++c) {
+          float4* at = reinterpret_cast<float4*>(grow + c * 4 * LPR + 4 * l);
+          const float4 more = *at;
+          q.v[2 * c] = add2(q.v[2 * c], pair(more.x, more.y));
+          q.v[2 * c + 1] = add2(q.v[2 * c + 1], pair(more.z, more.w));
+          if (LPR < 32) *at = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
       } else {
 #pragma unroll
-        for (int i = 0; i < NV / 2; ++i) q.v[u][i] = 0;
+        for (int i = 0; i < NV / 2; ++i) {
+          float* at = grow + 2 * i * LPR + l;
+          q.v[i] = add2(q.v[i], pair(at[0], at[LPR]));
+          if (LPR < 32) at[0] = at[LPR] = 0.f;
+        }
+      }
+      __syncwarp();
+      if (LPR == 32) {  // k <= 32: one slot a lane
+        if ((unsigned)q.id < (unsigned)a.E) grow[q.id] = 0.f;
+        __syncwarp();
       }
     }
+    if (in) {
+      float* out = a.dlogits + (unsigned)(t * a.E);
+      if constexpr (VEC) {
 #pragma unroll
-    for (int u = 0; u < RU; ++u) {
-      const int t = r0 + u * R::kGroups + g;
-      const bool in = t < last;
-      if (a.dw) {
-        // A step adds the slots j0 .. j0 + LPR - 1.  Ids are distinct in a token;
-        // should two slots of a step share one, the lower slot goes first.
-        for (int j0 = 0; j0 < a.k; j0 += LPR) {
-          int e = q.id[u];
-          float wj = q.w[u], dwj = q.dw[u];
-          if (LPR < 32 && j0 > 0) {
-            e = -1;
-            if (in && j0 + l < a.k) {
-              const unsigned at = t * a.k + j0 + l;
-              e = __ldg(a.idx + at), wj = __ldg(a.w + at), dwj = __ldg(a.dw + at);
-            }
-          }
-          if (in && j0 + l < a.k && (unsigned)e >= (unsigned)a.E) bad_id = true;
-          const bool has = (unsigned)e < (unsigned)a.E;
-          const float term = wj * (dwj - dotw[u]);
-          const unsigned same = __match_any_sync(0xffffffffu, has ? g * a.E + e : -1 - lane);
-          const int before = __popc(same & ((1u << lane) - 1u));
-          if (has && before == 0) grow[e] = LPR < 32 ? grow[e] + term : term;
-          __syncwarp();
-          for (int turn = 1; __any_sync(0xffffffffu, before >= turn); ++turn) {
-            if (has && before == turn) grow[e] += term;
-            __syncwarp();
-          }
+        for (int c = 0; c < NV / 4; ++c) {
+          const int e = c * 4 * LPR + 4 * l;
+          const float2 o0 = unpair(q.v[2 * c]), o1 = unpair(q.v[2 * c + 1]);
+          if (e < a.E)
+            __stcs(reinterpret_cast<float4*>(out + e), make_float4(o0.x, o0.y, o1.x, o1.y));
         }
-        if constexpr (VEC) {
+      } else {
 #pragma unroll
-          for (int c = 0; c < NV / 4; ++c) {
-            float4* at = reinterpret_cast<float4*>(grow + c * 4 * LPR + 4 * l);
-            const float4 more = *at;
-            q.v[u][2 * c] = add2(q.v[u][2 * c], pair(more.x, more.y));
-            q.v[u][2 * c + 1] = add2(q.v[u][2 * c + 1], pair(more.z, more.w));
-            if (LPR < 32) *at = make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < NV / 2; ++i) {
-            float* at = grow + 2 * i * LPR + l;
-            q.v[u][i] = add2(q.v[u][i], pair(at[0], at[LPR]));
-            if (LPR < 32) at[0] = at[LPR] = 0.f;
-          }
-        }
-        __syncwarp();
-        if (LPR == 32) {  // k <= 32: one slot a lane
-          if ((unsigned)q.id[u] < (unsigned)a.E) grow[q.id[u]] = 0.f;
-          __syncwarp();
-        }
-      }
-      if (in) {
-        float* out = a.dlogits + (unsigned)(t * a.E);
-        if constexpr (VEC) {
-#pragma unroll
-          for (int c = 0; c < NV / 4; ++c) {
-            const int e = c * 4 * LPR + 4 * l;
-            const float2 o0 = unpair(q.v[u][2 * c]), o1 = unpair(q.v[u][2 * c + 1]);
-            if (e < a.E)
-              __stcs(reinterpret_cast<float4*>(out + e), make_float4(o0.x, o0.y, o1.x, o1.y));
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < NV / 2; ++i) {
-            const int e = 2 * i * LPR + l;
-            const float2 o = unpair(q.v[u][i]);
-            if (e < a.E) __stcs(out + e, o.x);
-            if (e + LPR < a.E) __stcs(out + e + LPR, o.y);
-          }
+        for (int i = 0; i < NV / 2; ++i) {
+          const int e = 2 * i * LPR + l;
+          const float2 o = unpair(q.v[i]);
+          if (e < a.E) __stcs(out + e, o.x);
+          if (e + LPR < a.E) __stcs(out + e + LPR, o.y);
         }
       }
     }
   };
-  Rows even = {}, odd = {};
+  Row even = {}, odd = {};
   if constexpr (R::kAhead) {
-    if (first < last) load(even, first);
+    if (first < last) load(even, first + g);
     for (int r0 = first; r0 < last; r0 += 2 * kStep) {
-      load(odd, r0 + kStep);  // past the end: nothing is read or written
-      grad_rows(even, r0);
+      load(odd, r0 + kStep + g);  // past the end: nothing is read or written
+      grad_row(even, r0 + g);
       if (r0 + kStep >= last) break;
-      load(even, r0 + 2 * kStep);
-      grad_rows(odd, r0 + kStep);
+      load(even, r0 + 2 * kStep + g);
+      grad_row(odd, r0 + kStep + g);
     }
   } else {
     for (int r0 = first; r0 < last; r0 += kStep) {
-      load(even, r0);
-      grad_rows(even, r0);
+      load(even, r0 + g);
+      grad_row(even, r0 + g);
     }
   }
   if (bad_id) record_error(a.err, MOE_ERR_DEVICE_CHECK, 42);
@@ -861,11 +811,11 @@ __global__ void __launch_bounds__(256) k_combine_bwd(
 template <bool VEC, class F>
 cudaError_t with_columns(int E, F&& fn) {
   if (E <= 4) return fn(RowCfg<1, 4, VEC>{});
-  if (E <= 8) return fn(RowCfg<2, 4, VEC>{});
-  if (E <= 16) return fn(RowCfg<4, 4, VEC>{});
-  if (E <= 32) return fn(RowCfg<8, 4, VEC>{});
-  if (E <= 64) return fn(RowCfg<16, 4, VEC>{});
-  if (E <= 128) return fn(RowCfg<32, 4, VEC>{});
+  if (E <= 8) return fn(RowCfg<1, 8, VEC>{});
+  if (E <= 16) return fn(RowCfg<2, 8, VEC>{});
+  if (E <= 32) return fn(RowCfg<4, 8, VEC>{});
+  if (E <= 64) return fn(RowCfg<8, 8, VEC>{});
+  if (E <= 128) return fn(RowCfg<16, 8, VEC>{});
   if (E <= 256) return fn(RowCfg<32, 8, VEC>{});
   if (E <= 512) return fn(RowCfg<32, 16, VEC>{});
   return fn(RowCfg<32, 32, VEC>{});
@@ -920,7 +870,7 @@ cudaError_t launch_gate_bwd(const float* logits, const int* idx, const float* w,
     using R = decltype(cfg);
     // One run of whole groups for each warp that the SMs hold (two or four rounds of
     // shorter runs: 3% and 10% slower at 131072 x 256).
-    const long long warps = 8LL * R::kBlocks * sms;
+    const long long warps = 8LL * R::kGateBlocks * sms;
     long long rows = (s.T + warps - 1) / warps;
     rows = (rows + R::kGroups - 1) / R::kGroups * R::kGroups;
     a.rows_per_warp = (int)rows;
