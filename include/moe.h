@@ -454,7 +454,10 @@ MOE_API int moe_copy(void* dst, const void* src, int64_t bytes, void* stream);
  *   moe_gate_bwd                                 dw and the loss -> dlogits
  *   moe_router_bwd                               dlogits -> dw_g, dbias, dx
  *   moe_clip_grads                               any gradients, in one list
- * Every sum has a fixed order: equal inputs give equal bits.
+ * Every sum has a fixed order: equal inputs give equal bits.  fp32 and int32
+ * pointers need 4-byte alignment, bf16 ones 16-byte (gradient lists: 2-byte).
+ * Outputs must not overlap inputs or each other, but for a gradient of a list
+ * scaled in place.
  * ------------------------------------------------------------------------- */
 
 /* Bytes of workspace for moe_balance_loss, moe_gate_bwd and moe_router_bwd of
@@ -522,7 +525,8 @@ MOE_API int moe_gate_bwd(const float* logits, const int32_t* idx, const float* w
  *   without dw); w [T, k] fp32 in (may be NULL without dz);
  *   dw [T, k] fp32 out or NULL; dz [T*k, d] bf16 out or NULL, not both NULL.
  * A row index outside [0, T*k) gives dw = 0 and no row of dz; rows of dz that
- * no index names are left as they were. */
+ * no index names are left as they were; of two slots that name one row, either
+ * one's row may stay. */
 MOE_API int moe_combine_bwd(const moe_bf16* dy, const moe_bf16* z, const int32_t* row_of,
                             const float* w, const moe_shape* s, float* dw, moe_bf16* dz,
                             void* stream);
@@ -534,14 +538,21 @@ MOE_API int moe_combine_bwd(const moe_bf16* dy, const moe_bf16* z, const int32_t
  *   NULL without dx); dlogits [T, E] fp32 in;
  *   dw_g [d, E] fp32, dbias [E] fp32, dx [T, d] bf16 out, any of them NULL but
  *   not all.  Overwritten, not added to (T = 0 gives zeros).
+ * dw_g is an fp32 product's (dlogits as three bf16 planes, which hold 24 bits, on
+ * the tensor cores; sums in fp32).  For dx, which bf16 rounds to 2^-8, dlogits and
+ * w_g are rounded to fp16 (2^-11 of each value; rows scaled by powers of two, so
+ * that only values below 2^-28 of their row's largest lose more).  Where x,
+ * dlogits or w_g are not finite, so are the results they reach (NaN in place of
+ * some infinities).
  *   ws moe_workspace_size_bwd(s, 1) bytes */
 MOE_API int moe_router_bwd(const moe_bf16* x, const float* w_g, const float* dlogits,
                            const moe_shape* s, float* dw_g, float* dbias, moe_bf16* dx, void* ws,
                            void* stream);
 
 /* A gradient of a list: n elements, read from data and, scaled, written to
- * out (out == data: in place; otherwise the two must not overlap).  Both
- * aligned to their own element only. */
+ * out (out == data: in place; otherwise no out may overlap any data or other
+ * out of the list, and no gradient may be scaled in place twice).  Both aligned
+ * to their own element only. */
 typedef struct moe_grad {
   const void* data;  /* device memory; may be NULL if n == 0 */
   void* out;         /* device memory; NULL where only the norm is asked for */

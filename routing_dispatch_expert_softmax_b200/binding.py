@@ -671,9 +671,11 @@ class GradList:
     alignment) for moe_grad_sumsq / moe_grad_scale / moe_clip_grads, kept with
     its workspace so that a training loop marshals it once.  ``outs``: where
     the scaled gradients go, tensors of the same element counts, each of its
-    gradient's dtype or fp32; default: in place.  The tensors' addresses are
-    read again at every call; their dtypes and element counts are not.  As
-    with any workspace, calls on one GradList must not run concurrently."""
+    gradient's dtype or fp32; default: in place.  No out may share memory with
+    another gradient or out.  The tensors' addresses are read again at every
+    call; their dtypes and element counts are not.  As with any workspace, calls
+    on one GradList must not run concurrently, and come after its making in
+    stream order."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
@@ -711,6 +713,24 @@ class GradList:
             e.data = o.ptr(g, g.dtype, None, f"gradient {i}")
             e.out = o.ptr(out, out.dtype, None, f"out {i}")
             e.n, e.dtype, e.out_dtype = g.numel(), _GRAD_TYPES[g.dtype], _GRAD_TYPES[out.dtype]
+        # outs against everything else, by address
+        spans = []
+        for i, e in enumerate(self._entries):
+            if e.n:
+                spans.append((e.out, e.out + e.n * (2 if e.out_dtype else 4), i, True))
+                if e.data != e.out:
+                    spans.append((e.data, e.data + e.n * (2 if e.dtype else 4), i, False))
+        spans.sort()
+        end, who = 0, -1          # the span that reaches furthest so far
+        out_end, out_who = 0, -1  # ... of the outs alone
+        for lo, hi, i, is_out in spans:
+            if lo < out_end or (is_out and lo < end):
+                raise ValueError(f"GradList: the memory of out {i if is_out else out_who} "
+                                 f"overlaps that of entry {who if is_out else i}")
+            if hi > end:
+                end, who = hi, i
+            if is_out and hi > out_end:
+                out_end, out_who = hi, i
         self.index = o.index
         self.device = torch.device("cuda", o.index)
         self._seen = seen

@@ -532,8 +532,9 @@ int moe_gate_bwd(const float* logits, const int32_t* idx, const float* w, const 
 
 int moe_combine_bwd(const moe_bf16* dy, const moe_bf16* z, const int32_t* row_of, const float* w,
                     const moe_shape* s, float* dw, moe_bf16* dz, void* stream) {
-  if (!shape_ok(s) || (!dw && !dz)) return MOE_ERR_INVALID_ARG;
+  if (!shape_ok(s)) return MOE_ERR_INVALID_ARG;
   if (s->T == 0) return MOE_OK;
+  if (!dw && !dz) return MOE_ERR_INVALID_ARG;
   if (!ok16(dy) || !ok4(row_of)) return MOE_ERR_INVALID_ARG;
   if (dw && (!ok4(dw) || !ok16(z))) return MOE_ERR_INVALID_ARG;
   if (dz && (!ok16(dz) || !ok4(w))) return MOE_ERR_INVALID_ARG;
@@ -548,7 +549,7 @@ int moe_combine_bwd(const moe_bf16* dy, const moe_bf16* z, const int32_t* row_of
 
 int moe_router_bwd(const moe_bf16* x, const float* w_g, const float* dlogits, const moe_shape* s,
                    float* dw_g, float* dbias, moe_bf16* dx, void* ws, void* stream) {
-  if (!shape_ok(s) || (!dw_g && !dbias && !dx)) return MOE_ERR_INVALID_ARG;
+  if (!shape_ok(s) || (s->T > 0 && !dw_g && !dbias && !dx)) return MOE_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
   if ((dw_g && !aligned(dw_g, 4)) || (dbias && !aligned(dbias, 4))) return MOE_ERR_INVALID_ARG;
   if (s->T > 0 && (!ok4(dlogits) || (dw_g && !ok16(x)) || (dx && (!ok16(dx) || !ok4(w_g)))))

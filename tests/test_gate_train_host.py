@@ -209,6 +209,7 @@ def test_empty_batch_calls(lib):
     assert lib.moe_gate_bwd(None, None, None, None, None, None, 1, None, None, ref(T=0), 0.1, 0.1,
                             None, None, P, None) == moe.MOE_OK
     assert lib.moe_combine_bwd(None, None, None, None, ref(T=0), P, None, None) == moe.MOE_OK
+    assert lib.moe_combine_bwd(None, None, None, None, ref(T=0), None, None, None) == moe.MOE_OK
 
 
 def test_binding_refuses(lib):

@@ -623,6 +623,23 @@ def test_clip_list_follows_moved_tensors():
     assert torch.allclose(p, torch.full_like(p, 2.0 / (16 + 1e-6)), rtol=1e-6)
 
 
+def test_clip_refuses_shared_memory():
+    buf, other = torch.zeros(100, device=DEV), torch.zeros(100, device=DEV)
+    a, b = buf[:50], buf[40:]
+    with pytest.raises(ValueError, match="overlaps"):
+        moe.GradList([a, b])                       # both scaled in place
+    with pytest.raises(ValueError, match="overlaps"):
+        moe.GradList([a, a])
+    with pytest.raises(ValueError, match="overlaps"):
+        moe.GradList([a], [buf[10:60]])
+    with pytest.raises(ValueError, match="overlaps"):
+        moe.GradList([a, other[:50]], [buf[45:95], other[50:]])
+    with pytest.raises(ValueError, match="overlaps"):
+        moe.GradList([a, other[:60]], [other[10:60], buf[40:]])
+    moe.GradList([a, b], [other[:50], torch.zeros(60, device=DEV)])  # read twice only
+    moe.GradList([a, buf[50:]])
+
+
 def test_clip_nothing():
     norm = torch.ones(1, device=DEV)
     moe.moe_clip_grads([torch.empty(0, device=DEV)], 1.0, norm)

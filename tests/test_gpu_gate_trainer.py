@@ -166,6 +166,16 @@ def test_step_captured_and_replayed_beside_an_eager_one():
     assert torch.equal(y, y1) and torch.equal(g.dw_g, g1.dw_g)
 
 
+def test_step_of_no_tokens():
+    cfg, t, layer = make(4)
+    tr = moe.GateTrainer(layer, z_coef=1e-3)
+    y = tr(torch.empty(0, cfg.d, device=DEV).bfloat16())
+    assert y.shape == (0, cfg.d) and tr.loss.tolist() == [0, 0, 0] and not tr.counts.any()
+    g = tr.backward(torch.empty(0, cfg.d, device=DEV).bfloat16(), dx=True, dz=True, max_norm=1.0)
+    assert not g.dw_g.any() and g.norm.item() == 0.0 and g.dx.shape == (0, cfg.d)
+    assert tr.check() == moe.MOE_OK
+
+
 def test_refusals():
     cfg, t, layer = make(16)
     tr = moe.GateTrainer(layer)
