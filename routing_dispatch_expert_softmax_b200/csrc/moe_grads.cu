@@ -15,8 +15,9 @@ namespace {
 
 constexpr int kUnit = 2048;       // elements
 constexpr int kPiece = 32;        // most units of a block's run in one round
-constexpr int kSmallTable = 64;   // tensors of one launch: the small table, or
-constexpr int kGradTable = 768;   // the large one (24 KB of the 32 KB of a launch's parameters)
+// Tensors of one launch.  A table is copied with the launch, so a short list takes a
+// small one (2 or 8 KB); the largest has 24 of the 32 KB of a launch's parameters.
+constexpr int kTables[3] = {64, 256, 768};
 constexpr int kGradBlocks = 592;  // blocks of one launch (partial sums), 4 for each SM
 
 struct GradEntry {
@@ -372,7 +373,7 @@ cudaError_t scale_all(const moe_grad* g, int n, const double* sumsq, float max_n
 }  // namespace
 
 size_t grads_ws_bytes(int n) {
-  const size_t launches = (size_t)std::max(1, (n + kGradTable - 1) / kGradTable);
+  const size_t launches = (size_t)std::max(1, (n + kTables[2] - 1) / kTables[2]);
   return 256 + 256 + align_up(launches * kGradBlocks * sizeof(double), 256);
 }
 
@@ -381,14 +382,16 @@ double* grads_ws_sumsq(void* ws) {
 }
 
 cudaError_t launch_grad_sumsq(const moe_grad* g, int n, double* out, void* ws, cudaStream_t st) {
-  return n <= kSmallTable ? sumsq<kSmallTable>(g, n, out, ws, st)
-                          : sumsq<kGradTable>(g, n, out, ws, st);
+  return n <= kTables[0]   ? sumsq<kTables[0]>(g, n, out, ws, st)
+         : n <= kTables[1] ? sumsq<kTables[1]>(g, n, out, ws, st)
+                           : sumsq<kTables[2]>(g, n, out, ws, st);
 }
 
 cudaError_t launch_grad_scale(const moe_grad* g, int n, const double* sumsq, float max_norm,
                               float* norm, cudaStream_t st) {
-  return n <= kSmallTable ? scale_all<kSmallTable>(g, n, sumsq, max_norm, norm, st)
-                          : scale_all<kGradTable>(g, n, sumsq, max_norm, norm, st);
+  return n <= kTables[0]   ? scale_all<kTables[0]>(g, n, sumsq, max_norm, norm, st)
+         : n <= kTables[1] ? scale_all<kTables[1]>(g, n, sumsq, max_norm, norm, st)
+                           : scale_all<kTables[2]>(g, n, sumsq, max_norm, norm, st);
 }
 
 }  // namespace moe
