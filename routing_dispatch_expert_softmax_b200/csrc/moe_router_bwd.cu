@@ -204,6 +204,7 @@ struct RouterGemmArgs {
   int dw_items, dx_items;
   int ne, nd;            // expert and column tiles of dW
   int sets, parts;       // RouterPlanes
+  int rb;                // tiles of the B ring
   int kblocks, kper;     // 64-token blocks in all, and of one range
   int mt;                // token tiles of dx
   int kx;                // 64-expert blocks of dx
@@ -231,7 +232,7 @@ constexpr int kChunk = 2;
 constexpr int kRA = 4, kRB = 4;
 constexpr int kATile = 128 * 64 * 2, kBTile = 256 * 64 * 2;
 constexpr int kStageOut = 2 * 32 * 64;  // per epilogue warp: two times 32 rows x 32 bf16 of dx
-constexpr int kRouterSmem = kRA * kATile + kRB * kBTile + 8 * kStageOut + 1024 + 256;
+constexpr int router_smem(int rb) { return kRA * kATile + rb * kBTile + 8 * kStageOut + 1024 + 256; }
 constexpr int kRouterThreads = 320;  // TMA, MMA and eight epilogue warps
 
 // Descriptor of an MN-major operand tile with 128-byte swizzle: blocks of 64
@@ -297,7 +298,8 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sa = smem;
   uint8_t* sb = smem + kRA * kATile;
-  uint8_t* so = sb + kRB * kBTile;
+  const int rb = args.rb;
+  uint8_t* so = sb + rb * kBTile;
   uint64_t* a_full = reinterpret_cast<uint64_t*>(so + 8 * kStageOut);
   uint64_t* a_empty = a_full + kRA;
   uint64_t* b_full = a_empty + kRA;
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
           uint8_t* dst = take_b();
           if (!(ok = dst != nullptr)) break;
           tma_load_3d(dst, &tm_x, &b_full[b.slot], 0, kb * 64, dt * 4);
-          b.next(kRB);
+          b.next(rb);
           for (int p = args.sets - 1; p >= 0; --p) {
             dst = take_a();
             if (!(ok = dst != nullptr)) break;
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
       }
       int nt = dx0 / args.mt, mt = dx0 - nt * args.mt;
       for (int w = dx0; w < dx1 && ok; ++w) {
-        const bool load_b = args.kx > kRB || w == dx0 || mt == 0;
+        const bool load_b = args.kx > rb || w == dx0 || mt == 0;
         for (int kb = 0; kb < args.kx && ok; ++kb) {
           uint8_t* dst = take_a();
           if (!(ok = dst != nullptr)) break;
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
           dst = take_b();
           if (!(ok = dst != nullptr)) break;
           tma_load_2d(dst, &tm_w, &b_full[b.slot], kb * 64, nt * 256, policy);
-          b.next(kRB);
+          b.next(rb);
         }
         if (++mt == args.mt) mt = 0, ++nt;
       }
@@ -449,14 +451,14 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
               a.next(kRA);
             }
             umma_commit(&b_empty[b.slot]);
-            b.next(kRB);
+            b.next(rb);
           }
           if (ok) umma_commit(&tfull[ab]);
         }
       }
       // W's tiles stay until the last item of a block of columns (or, with too
       // many experts for the ring, are new for each item).
-      const bool keep = args.kx <= kRB;
+      const bool keep = args.kx <= rb;
       Ring b0;
       int mt = dx0 < dx1 ? dx0 % args.mt : 0;
       for (int w = dx0; w < dx1 && ok; ++w, ++it) {
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
           umma_commit(&a_empty[a.slot]);
           a.next(kRA);
           if (free_b) umma_commit(&b_empty[b.slot]);
-          b.next(kRB);
+          b.next(rb);
         }
         if (ok) umma_commit(&tfull[ab]);
       }
@@ -735,6 +737,7 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
     RouterGemmArgs a{};
     a.T = T, a.d = d, a.E = E;
     a.sets = pl.sets, a.parts = pl.parts;
+    a.rb = cp <= 128 ? 3 : kRB;
     a.ne = apart ? (E + 127) / 128 : 1, a.nd = (d + 255) / 256;
     a.kblocks = kblocks, a.kper = kper;
     a.dw_items = dw ? a.ne * a.nd * ranges : 0;
@@ -773,11 +776,11 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if (dev >= 128 || !(ready[dev / 64].load(std::memory_order_acquire) >> (dev % 64) & 1)) {
       e = cudaFuncSetAttribute(k_router_gemm, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kRouterSmem);
+                               router_smem(kRB));
       if (e != cudaSuccess) return e;
       if (dev < 128) ready[dev / 64].fetch_or(1ull << (dev % 64), std::memory_order_release);
     }
-    e = launch_kernel(k_router_gemm, dim3(grid), dim3(kRouterThreads), kRouterSmem, st, 1, mx, mn,
+    e = launch_kernel(k_router_gemm, dim3(grid), dim3(kRouterThreads), router_smem(a.rb), st, 1, mx, mn,
                       mk, mw, mdx, a);
     if (e != cudaSuccess) return e;
   }
