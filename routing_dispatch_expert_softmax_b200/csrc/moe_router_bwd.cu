@@ -15,6 +15,12 @@
 // One persistent kernel then runs the tiles of both products.  The tokens are
 // the long axis of dW, so its tiles split over token ranges; a last kernel
 // adds the ranges' partial tiles in order.
+//
+// 16384 x 7168 x 256: 215 us (240 GFLOP of 16-bit products: dW's three, dx's one),
+// of which the products take 182 with the tensor pipe 66% active, and 253 us back to
+// back, where the power limit sets the clock.  8192 x 2048 x 128: 37 us, the products
+// 22 (a third of it MMAs; the rest is each item's start and end, 2 us, and dx's way
+// out through TMEM), the operands' kernel 5 and the sum 4.
 #include <cuda_fp16.h>
 
 #include <atomic>
