@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV, VEC>::kGateBlocks) k_gate
 // are neighbours, so dy's row comes from L1 for all but the first of them.  A row
 // index outside [0, T*k) gives dw = 0 and writes nothing.
 // Bound by HBM: 8192 x 2048, k = 8, dw and dz: 96 us (6.0 TB/s); 10294 x 64, k = 13,
-// dw alone: 38 us with a warp for each row of 128 bytes, 14 with 8 lanes.
+// dw alone: 38 us with a warp for each row of 128 bytes, 9 with 8 lanes.
 template <int G, bool DW, bool DZ>
 __global__ void __launch_bounds__(256) k_combine_bwd(
     const __nv_bfloat16* __restrict__ dy, const __nv_bfloat16* __restrict__ z,
