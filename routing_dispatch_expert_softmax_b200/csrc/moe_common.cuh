@@ -255,7 +255,8 @@ inline int router_range_blocks(const moe_shape& s, bool dx) {
   const double dx_us = dx ? (double)((s.T + 127) / 128) * cols * router_dx_tile_us(s.E) : 0.0;
   long long best = std::max(1LL, blocks);
   double least = 0.0;
-  for (long long r = 1; r <= std::min(blocks, 148LL); ++r) {
+  // (1 to 8 one by one, then steps of an eighth: this runs on the host in every call)
+  for (long long r = 1; r <= std::min(blocks, 148LL); r += std::max(1LL, r / 8)) {
     const long long per = (blocks + r - 1) / r, n = (blocks + per - 1) / per;
     const double waves = (double)((tiles * n + 147) / 148);
     const double us = std::max(waves * (per * kb + kRouterItemUs),

@@ -634,52 +634,52 @@ __global__ void __launch_bounds__(256) k_router_sum(const float* __restrict__ pa
   __shared__ float4 meet[G > 1 ? 256 : 1];
   pdl_trigger();
   pdl_wait();
-  if ((int)blockIdx.x < dw_blocks) {
-    // n is a multiple of 64 (d is); dw itself may be aligned to 4 bytes only
-    constexpr int kSpan = 256 / G;
-    const int c = threadIdx.x % kSpan, g = threadIdx.x / kSpan;
-    const long long i = (long long)blockIdx.x * kSpan + c, n4 = n / 4;
-    const float4* p4 = reinterpret_cast<const float4*>(part) + i;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < n4) {
+  if ((int)blockIdx.x >= dw_blocks) {
+    const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
+    const int e = ((int)blockIdx.x - dw_blocks) * 8 + c;
+    double s = 0.0;
+    if (e < E) {
 #pragma unroll 8
-      for (int p = g; p < partials; p += G) {
-        const float4 v = __ldcs(p4 + p * n4);
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-      }
+      for (int r = g; r < sum_rows; r += 32) s += sums[(size_t)r * E + e];
     }
-    if (G > 1) {
-      meet[threadIdx.x] = s;
-      __syncthreads();
-      if (g > 0) return;
+    red[g][c] = s;
+    __syncthreads();
+    if (g == 0 && e < E) {
+      s = 0.0;
 #pragma unroll
-      for (int k = 1; k < G; ++k) {
-        const float4 v = meet[k * kSpan + c];
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-      }
-    }
-    if (i >= n4) return;
-    if ((reinterpret_cast<uintptr_t>(dw) & 15) == 0) {
-      reinterpret_cast<float4*>(dw)[i] = s;
-    } else {
-      dw[4 * i] = s.x, dw[4 * i + 1] = s.y, dw[4 * i + 2] = s.z, dw[4 * i + 3] = s.w;
+      for (int i = 0; i < 32; ++i) s += red[i][c];
+      db[e] = (float)s;
     }
     return;
   }
-  const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
-  const int e = ((int)blockIdx.x - dw_blocks) * 8 + c;
-  double s = 0.0;
-  if (e < E) {
+  // n is a multiple of 64 (d is); dw itself may be aligned to 4 bytes only
+  constexpr int kSpan = 256 / G;
+  const int c = threadIdx.x % kSpan, g = threadIdx.x / kSpan;
+  const long long i = (long long)blockIdx.x * kSpan + c, n4 = n / 4;
+  const float4* p4 = reinterpret_cast<const float4*>(part) + i;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (i < n4) {
 #pragma unroll 8
-    for (int r = g; r < sum_rows; r += 32) s += sums[(size_t)r * E + e];
+    for (int p = g; p < partials; p += G) {
+      const float4 v = __ldcs(p4 + p * n4);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
   }
-  red[g][c] = s;
-  __syncthreads();
-  if (g == 0 && e < E) {
-    s = 0.0;
+  if (G > 1) {
+    meet[threadIdx.x] = s;
+    __syncthreads();
+    if (g > 0) return;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += red[i][c];
-    db[e] = (float)s;
+    for (int k = 1; k < G; ++k) {
+      const float4 v = meet[k * kSpan + c];
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+  }
+  if (i >= n4) return;
+  if ((reinterpret_cast<uintptr_t>(dw) & 15) == 0) {
+    reinterpret_cast<float4*>(dw)[i] = s;
+  } else {
+    dw[4 * i] = s.x, dw[4 * i + 1] = s.y, dw[4 * i + 2] = s.z, dw[4 * i + 3] = s.w;
   }
 }
 
