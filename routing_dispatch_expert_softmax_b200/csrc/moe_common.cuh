@@ -239,13 +239,15 @@ constexpr double kRouterItemUs = 2.0;
 // (eight of them at a time from 16 partials on).
 inline double router_partial_us(const moe_shape& s, int parts, long long ranges) {
   const long long n = parts * ranges;
-  return 8.0 * n * s.d * s.E / 5e6 + (n > 1 ? 2.5 : 0.0) + 0.1 * (n < 16 ? n : n / 8.0);
+  return 8.0 * n * s.d * s.E / 1e7 + (n > 1 ? 2.5 : 0.0) + 0.1 * (n < 16 ? n : n / 8.0);
 }
 
 // The tokens of dW are cut into ranges: more of them fill the SMs, but each
 // writes partials that are read again.  The time of `r` ranges: all work over
-// 148 SMs, but no less than the longest SM's dW items, plus each partial's way to L2 and back.  The r with the least
-// time is taken; what is returned is the 64-token blocks of one range.
+// 148 SMs, but no less than the longest SM's dW items; a share of that longest,
+// since long items leave the rest uneven; and the partials'.  The r with the least
+// time is taken (over eight shapes within 4% of the best one); what is returned is
+// the 64-token blocks of one range.
 inline int router_range_blocks(const moe_shape& s, bool dx) {
   const RouterPlanes pl = router_planes(s.E, s.T);
   const double kb = router_dw_block_us(pl.sets);
@@ -259,9 +261,10 @@ inline int router_range_blocks(const moe_shape& s, bool dx) {
   for (long long r = 1; r <= std::min(blocks, 148LL); r += std::max(1LL, r / 8)) {
     const long long per = (blocks + r - 1) / r, n = (blocks + per - 1) / per;
     const double waves = (double)((tiles * n + 147) / 148);
-    const double us = std::max(waves * (per * kb + kRouterItemUs),
-                               (tiles * (blocks * kb + n * kRouterItemUs) + dx_us) / 148) +
-                      router_partial_us(s, pl.parts, n);
+    const double longest = waves * (per * kb + kRouterItemUs);
+    const double all = (tiles * (blocks * kb + n * kRouterItemUs) + dx_us) / 148;
+    const double us =
+        std::max(longest, all) + 0.15 * longest + router_partial_us(s, pl.parts, n);
     if (r == 1 || us < least) best = per, least = us;
   }
   return (int)best;
