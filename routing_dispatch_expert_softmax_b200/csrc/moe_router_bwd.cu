@@ -639,8 +639,14 @@ __global__ void __launch_bounds__(256) k_router_sum(const float* __restrict__ pa
     const int e = ((int)blockIdx.x - dw_blocks) * 8 + c;
     double s = 0.0;
     if (e < E) {
-#pragma unroll 8
-      for (int r = g; r < sum_rows; r += 32) s += sums[(size_t)r * E + e];
+      for (int r = g; r < sum_rows; r += 256) {
+        float v[8];  // eight loads in flight
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = r + 32 * i < sum_rows ? __ldg(sums + (size_t)(r + 32 * i) * E + e) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += v[i];
+      }
     }
     red[g][c] = s;
     __syncthreads();
