@@ -279,8 +279,7 @@ inline BwdLayout bwd_layout(const moe_shape& s, int S) {
     o = align_up(o + bytes, 256);
     return at;
   };
-  // One sequence of up to 64 tokens: one block, which then needs no second kernel.
-  // Else 32 tokens a block (4 for each warp), or the tokens of an average sequence (a
+  // One sequence of up to 64 tokens: one block.  Else 32 tokens a block (4 for each warp), or the tokens of an average sequence (a
   // block takes the sequences in its tokens one after the other), until the SMs are
   // full, with four blocks (three above 256 experts, two above 512) each.
   const long long nblk = E <= 256 ? 592 : E <= 512 ? 444 : 296;

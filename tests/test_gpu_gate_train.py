@@ -161,7 +161,8 @@ def check_bwd(b, gates=True, aux=True):
 
 SIZES = [(1, 1, 1), (1, 2, 1), (3, 4, 4), (64, 8, 2), (33, 5, 3), (17, 13, 13), (31, 24, 7),
          (5, 33, 8), (40, 64, 6), (257, 100, 8), (129, 128, 8), (70, 130, 9), (61, 256, 8),
-         (37, 300, 32), (20, 512, 5), (11, 1000, 32), (9, 1024, 8)]
+         (37, 300, 32), (20, 512, 5), (11, 1000, 32), (9, 1024, 8), (1000, 6, 2), (2000, 33, 4),
+         (1030, 256, 8), (300, 700, 3)]
 
 
 @pytest.mark.parametrize("T,E,k", SIZES)
