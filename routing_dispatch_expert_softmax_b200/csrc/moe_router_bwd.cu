@@ -14,11 +14,11 @@
 //       those below 2^-28 of the row's largest lose bits; the epilogue scales back.
 // One persistent kernel then runs the tiles of both products.  The tokens are
 // the long axis of dW, so its tiles split over token ranges; a last kernel
-// adds the ranges' partial tiles in order.
+// adds the ranges' partial tiles in order.  Few tokens take one kernel of their own.
 //
-// 16384 x 7168 x 256: 215 us (240 GFLOP of 16-bit products: dW's three, dx's one),
-// of which the products take 182 with the tensor pipe 66% active, and 253 us back to
-// back, where the power limit sets the clock.  8192 x 2048 x 128: 37 us, the products
+// 16384 x 7168 x 256: 210 us (240 GFLOP of 16-bit products: dW's three, dx's one),
+// of which the products take 182 with the tensor pipe 66% active, and 247 us back to
+// back, where the power limit sets the clock.  8192 x 2048 x 128: 34.5 us, the products
 // 22 (a third of it MMAs; the rest is each item's start and end, 2 us, and dx's way
 // out through TMEM), the operands' kernel 5 and the sum 4.
 #include <cuda_fp16.h>
@@ -689,6 +689,205 @@ __global__ void __launch_bounds__(256) k_router_sum(const float* __restrict__ pa
   }
 }
 
+// ============================================================== few tokens
+// Up to 64 tokens the products are small (64 x 2048 x 128: 134 MFLOP) and the time is
+// launches, loads and stores, so all of it is one kernel and warp-wide MMAs on
+// fragments made in registers: the tcgen05 tiles want their operands laid out by a
+// kernel before.  A block takes 16 columns of d, with dL [T][E], its W [16][E] and its
+// x [T][16] in shared memory.
+//   dW: 16 columns x 8 experts a tile, K = tokens, x in bf16, dL in three bf16 planes
+//       with a sum each, added last;
+//   dx: 16 tokens x 8 columns a tile, K = experts, both rounded to tf32 (2^-11 of each
+//       value, as fp16 keeps in the large path; no scaling, tf32 has fp32's range).
+// Rows lie ep = 4 (mod 32) words apart: the 8 x 4 lanes of a fragment hit 32 banks.
+// Every block reads all of dL from L2, which is most of the time (64 x 2048 x 128: 7.5
+// us, 4.4 with 16 tokens; 8 warps a block took 10.8, 16 as here hide more of it).
+struct RouterSmallArgs {
+  const __nv_bfloat16* x;
+  const float* w;
+  const float* dl;
+  float* dw;
+  float* db;
+  __nv_bfloat16* dx;
+  int T, d, E, ep, vec_dl, vec_w;
+};
+constexpr int kSmallT = 64, kSmallXPitch = 24, kSmallWarps = 16;  // bf16 of one token of x in shared memory
+
+// rows x cols of src into rows of ep words, zeros up to rows_all x cols_all.
+__device__ __forceinline__ void copy_rows(float* dst, const float* __restrict__ src, int rows,
+                                          int cols, int rows_all, int cols_all, int ep, int vec) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = warp; r < rows_all; r += kSmallWarps) {
+    float* to = dst + r * ep;
+    const float* from = src + (size_t)r * cols;
+    const int n = r < rows ? cols : 0;
+    if (vec) {
+      for (int c = 4 * lane; c < n; c += 128)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + c)), "l"(from + c)
+                     : "memory");
+    } else {
+      for (int c = lane; c < n; c += 32)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to + c)), "l"(from + c)
+                     : "memory");
+    }
+    for (int c = n + lane; c < cols_all; c += 32) to[c] = 0.f;
+  }
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t to_tf32(float v) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ uint32_t pair_of(__nv_bfloat16 lo, __nv_bfloat16 hi) {
+  const __nv_bfloat162 v = __halves2bfloat162(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__global__ void __launch_bounds__(32 * kSmallWarps) k_router_bwd_small(const RouterSmallArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  const int T16 = (a.T + 15) / 16 * 16, E8 = (a.E + 7) / 8 * 8;
+  float* sdl = sm;                                                   // [T16][ep]
+  float* sw = sdl + (size_t)T16 * a.ep;                              // [16][ep]
+  float* meet = sw + 16 * a.ep;                                      // [8 warps][16][16]
+  __nv_bfloat16* sx = reinterpret_cast<__nv_bfloat16*>(meet + 256 * kSmallWarps);  // [T16][kSmallXPitch]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t4 = lane & 3;  // a fragment's row or column, and place in it
+  pdl_trigger();
+  pdl_wait();
+  const int i0 = blockIdx.x * 16;
+  copy_rows(sdl, a.dl, a.T, a.E, T16, E8, a.ep, a.vec_dl);
+  if (a.dx) copy_rows(sw, a.w + (size_t)i0 * a.E, 16, a.E, 16, E8, a.ep, a.vec_w);
+  if (a.dw)
+    for (int q = threadIdx.x; q < 2 * T16; q += 32 * kSmallWarps) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (q < 2 * a.T)
+        v = __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)(q >> 1) * a.d + i0) + (q & 1));
+      *reinterpret_cast<uint4*>(sx + (q >> 1) * kSmallXPitch + (q & 1) * 8) = v;
+    }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+
+  if (a.dw) {
+    uint32_t xa[kSmallT / 16][4];
+#pragma unroll
+    for (int ks = 0; ks < kSmallT / 16; ++ks) {
+      if (16 * ks >= T16) break;
+      const __nv_bfloat16* p = sx + (16 * ks + 2 * t4) * kSmallXPitch + g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // rows g, g + 8; tokens 2 t4, + 8
+        const __nv_bfloat16* q = p + (i >> 1) * 8 * kSmallXPitch + (i & 1) * 8;
+        xa[ks][i] = pair_of(q[0], q[kSmallXPitch]);
+      }
+    }
+    const bool even = a.E % 2 == 0 && (reinterpret_cast<uintptr_t>(a.dw) & 7) == 0;
+    for (int nt = warp; nt < E8 / 8; nt += kSmallWarps) {
+      float c[4] = {}, cm[4] = {}, cl[4] = {};
+#pragma unroll
+      for (int ks = 0; ks < kSmallT / 16; ++ks) {
+        if (16 * ks >= T16) break;
+        const float* p = sdl + (16 * ks + 2 * t4) * a.ep + 8 * nt + g;
+        const Split3 v0 = split3(p[0]), v1 = split3(p[a.ep]);
+        const Split3 v2 = split3(p[8 * a.ep]), v3 = split3(p[9 * a.ep]);
+        mma_bf16(cl, xa[ks], pair_of(v0.lo, v1.lo), pair_of(v2.lo, v3.lo));
+        mma_bf16(cm, xa[ks], pair_of(v0.mid, v1.mid), pair_of(v2.mid, v3.mid));
+        mma_bf16(c, xa[ks], pair_of(v0.hi, v1.hi), pair_of(v2.hi, v3.hi));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] += cm[i] + cl[i];
+      const int e = 8 * nt + 2 * t4;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float* out = a.dw + (size_t)(i0 + g + 8 * h) * a.E + e;
+        if (even && e < a.E) {
+          *reinterpret_cast<float2*>(out) = make_float2(c[2 * h], c[2 * h + 1]);
+        } else {
+          if (e < a.E) out[0] = c[2 * h];
+          if (e + 1 < a.E) out[1] = c[2 * h + 1];
+        }
+      }
+    }
+  }
+  if (a.dx) {
+    // a warp takes 16 tokens, and with fewer than 8 such tiles a part of the experts
+    const int tiles = T16 / 16, parts = kSmallWarps / tiles, mt = warp % tiles, part = warp / tiles;
+    float c[2][4] = {};
+    if (part < parts) {
+      const int n8 = E8 / 8;
+      const float* pa = sdl + (16 * mt + g) * a.ep + t4;
+      const float* pb = sw + g * a.ep + t4;
+#pragma unroll 4
+      for (int k = part; k < n8; k += parts) {
+        uint32_t f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = to_tf32(pa[(i & 1) * 8 * a.ep + 8 * k + (i >> 1) * 4]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float* q = pb + 8 * n * a.ep + 8 * k;
+          mma_tf32(c[n], f, to_tf32(q[0]), to_tf32(q[4]));
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        meet[warp * 256 + (g + (i >> 1) * 8) * 16 + 8 * n + 2 * t4 + (i & 1)] = c[n][i];
+    __syncthreads();
+    for (int q = threadIdx.x; q < 8 * a.T; q += 32 * kSmallWarps) {  // a pair of columns each
+      const int t = q >> 3, i = 2 * (q & 7);
+      float s0 = 0.f, s1 = 0.f;
+      for (int p = 0; p < parts; ++p) {
+        const float2 v = *reinterpret_cast<const float2*>(
+            meet + (p * tiles + t / 16) * 256 + (t % 16) * 16 + i);
+        s0 += v.x, s1 += v.y;
+      }
+      *reinterpret_cast<uint32_t*>(a.dx + (size_t)t * a.d + i0 + i) = pack_bf16x2(s0, s1);
+    }
+  }
+  if (a.db)  // each block some experts
+    for (int e = blockIdx.x * 32 * kSmallWarps + threadIdx.x; e < a.E; e += gridDim.x * 32 * kSmallWarps) {
+      float s = 0.f;
+#pragma unroll 8
+      for (int r = 0; r < a.T; ++r) s += sdl[r * a.ep + e];
+      a.db[e] = s;
+    }
+}
+
+constexpr int kSmallSmem = 113 * 1024;  // two blocks an SM
+
+int router_small_ep(int E) { return ((E + 7) / 8 * 8 + 27) / 32 * 32 + 4; }
+size_t router_small_smem(const moe_shape& s) {
+  const size_t T16 = (s.T + 15) / 16 * 16;
+  return sizeof(float) * ((T16 + 16) * router_small_ep(s.E) + 256 * kSmallWarps) +
+         2 * T16 * kSmallXPitch;
+}
+// Where the blocks of 16 columns fit the GPU at once: E = 8 to 256, d = 512 to 4096, 4
+// to 64 tokens took 3.1 to 12.3 us where the three kernels took 7.6 to 14.2, less in
+// each of 48.  In a second wave (d = 7168) each block loads dL again: 4 and 16 tokens
+// still won (5.6 to 10.3 against 8.1 to 12.7), 32 lost at two of four E, 64 at all (20.9
+// against 15.3 with 256 experts).
+bool router_small(const moe_shape& s, int sms) {
+  return s.T <= kSmallT && s.d / 16 <= (s.T <= 16 ? 4 : 2) * sms &&
+         router_small_smem(s) <= kSmallSmem;
+}
+
 // 16-bit tensor map of up to 4 dimensions, innermost first; strides in bytes of dimensions 1 and up.
 bool make_map(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
               const uint64_t* strides, const uint32_t* box,
@@ -704,12 +903,40 @@ bool make_map(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
          CUDA_SUCCESS;
 }
 
+// Raises a kernel's dynamic shared memory limit once for each device (the attribute
+// belongs to the device's copy of the kernel); `ready` has a bit for each.
+typedef std::atomic<uint64_t> DeviceBits[2];
+DeviceBits gemm_ready, small_ready;
+template <class K>
+cudaError_t allow_smem(K kern, int bytes, DeviceBits& ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev < 128;
+  if (known && (ready[dev / 64].load(std::memory_order_acquire) >> (dev % 64) & 1)) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known)
+    ready[dev / 64].fetch_or(1ull << (dev % 64), std::memory_order_release);
+  return e;
+}
+
 }  // namespace
 
 cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const float* dl,
                               const moe_shape& s, float* dw, float* db, __nv_bfloat16* dx,
                               const BwdLayout& L, char* ws, int sms, cudaStream_t st) {
   const int T = s.T, d = s.d, E = s.E, cp = L.cp;
+  const auto vec = [&](const float* p) {
+    return (int)(E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0);
+  };
+  const bool products = dw || dx;
+  if (products && router_small(s, sms)) {
+    cudaError_t e = allow_smem(k_router_bwd_small, kSmallSmem, small_ready);
+    if (e != cudaSuccess) return e;
+    const RouterSmallArgs a{x, w_g, dl, dw, db, dx, T, d, E, router_small_ep(E), vec(dl), vec(w_g)};
+    return launch_kernel(k_router_bwd_small, dim3(d / 16), dim3(32 * kSmallWarps),
+                         router_small_smem(s), st, 1, a);
+  }
   __nv_bfloat16* dlp = reinterpret_cast<__nv_bfloat16*>(ws + L.dl_planes);
   __half* dlh = reinterpret_cast<__half*>(ws + L.dl_half);
   __half* wh = reinterpret_cast<__half*>(ws + L.w_half);
@@ -717,10 +944,6 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
   __nv_bfloat16* w_back = reinterpret_cast<__nv_bfloat16*>(ws + L.w_back);
   float* sums = reinterpret_cast<float*>(ws + L.db_part);
   float* part = reinterpret_cast<float*>(ws + L.dw_part);
-  const bool products = dw || dx;
-  const auto vec = [&](const float* p) {
-    return (int)(E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0);
-  };
   const RouterPlanes pl = router_planes(E, T);
   const bool apart = pl.sets == 3;  // each plane for itself, or side by side in a row of four
   const long long prow = apart ? pl.width : 4 * pl.width;
@@ -782,16 +1005,7 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
     if (dx && (!make_map(&mk, dlh, 2, kd, &row, kb) || !make_map(&mw, wh, 2, wd, &row, wb) ||
                !make_map(&mdx, dx, 2, od, os, ob, CU_TENSOR_MAP_SWIZZLE_64B)))
       return cudaErrorInvalidValue;
-    // Once for each device: the attribute belongs to the device's copy of the kernel.
-    static std::atomic<uint64_t> ready[2];
-    int dev = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if (dev >= 128 || !(ready[dev / 64].load(std::memory_order_acquire) >> (dev % 64) & 1)) {
-      e = cudaFuncSetAttribute(k_router_gemm, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               router_smem(kRB));
-      if (e != cudaSuccess) return e;
-      if (dev < 128) ready[dev / 64].fetch_or(1ull << (dev % 64), std::memory_order_release);
-    }
+    if ((e = allow_smem(k_router_gemm, router_smem(kRB), gemm_ready)) != cudaSuccess) return e;
     e = launch_kernel(k_router_gemm, dim3(grid), dim3(kRouterThreads), router_smem(a.rb), st, 1, mx, mn,
                       mk, mw, mdx, a);
     if (e != cudaSuccess) return e;

@@ -457,6 +457,51 @@ def test_router_bwd_tiny_and_huge_gradients():
     check_router(100, 64, 16, scale=1e30)
 
 
+@pytest.mark.parametrize("T", [1, 7, 15, 16, 17, 32, 33, 63, 64, 65])
+@pytest.mark.parametrize("d,E", [(64, 1), (64, 3), (128, 8), (448, 60), (1088, 130), (4672, 36), (4736, 9), (4800, 16),
+                                 (64, 255), (128, 260), (64, 640), (9472, 5), (9536, 5)])
+def test_router_bwd_few_tokens(T, d, E):
+    check_router(T, d, E)
+
+
+@pytest.mark.parametrize("which", [(1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 0, 1), (0, 1, 1)])
+@pytest.mark.parametrize("T", [5, 50])
+def test_router_bwd_few_tokens_parts(T, which):
+    check_router(T, 192, 24, *map(bool, which))
+
+
+@pytest.mark.parametrize("scale", [1e-30, 3e-34, 1e30])
+def test_router_bwd_few_tokens_tiny_and_huge_gradients(scale):
+    check_router(40, 128, 20, scale=scale)
+
+
+def test_router_bwd_few_tokens_same_bits_and_unaligned():
+    x, W, dl, s, ws, out = check_router(37, 256, 12)
+    want = {n: t.clone() for n, t in out.items()}
+    # dlogits and the fp32 outputs may start on any element
+    dl1 = torch.empty(dl.numel() + 1, device=DEV)[1:].view_as(dl).copy_(dl)
+    W1 = torch.empty(W.numel() + 1, device=DEV)[1:].view_as(W).copy_(W)
+    buf = torch.full((out["dw_g"].numel() + 2,), 7.0, device=DEV)
+    out1 = dict(out, dw_g=buf[1:-1].view_as(W))
+    for _ in range(3):
+        moe.moe_router_bwd(x, W1, dl1, s, ws, **out1)
+        assert all(torch.equal(want[n], out1[n]) for n in want)
+    assert buf[0] == 7 and buf[-1] == 7
+
+
+def test_router_bwd_few_tokens_infinite_gradient_shows():
+    x, W, dl, s, ws, out = check_router(20, 64, 8)
+    dl[3, 2] = math.inf
+    dl[5, 4] = math.nan
+    moe.moe_router_bwd(x, W, dl, s, ws, **out)
+    for e in (2, 4):
+        assert not torch.isfinite(out["dw_g"][:, e]).any() and not torch.isfinite(out["dbias"][e])
+    good = [0, 1, 3, 5, 6, 7]
+    assert torch.isfinite(out["dw_g"][:, good]).all() and torch.isfinite(out["dbias"][good]).all()
+    assert not torch.isfinite(out["dx"][[3, 5]]).any()
+    assert torch.isfinite(out["dx"][[0, 1, 2, 4, 19]]).all()
+
+
 def test_router_bwd_no_tokens():
     s = MoEShape.of(0, 128, 8, 1, 64)
     ws = moe.workspace_bwd(s)
