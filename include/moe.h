@@ -540,10 +540,10 @@ MOE_API int moe_combine_bwd(const moe_bf16* dy, const moe_bf16* z, const int32_t
  *   not all.  Overwritten, not added to (T = 0 gives zeros).
  * dw_g is an fp32 product's (dlogits as three bf16 planes, which hold 24 bits, on
  * the tensor cores; sums in fp32).  For dx, which bf16 rounds to 2^-8, dlogits and
- * w_g are rounded to fp16 (2^-11 of each value; rows scaled by powers of two, so
- * that only values below 2^-28 of their row's largest lose more).  Where x,
- * dlogits or w_g are not finite, so are the results they reach (NaN in place of
- * some infinities).
+ * w_g are rounded to 2^-11 of each value: with few tokens to tf32, else to fp16
+ * (rows scaled by powers of two, so that only values below 2^-28 of their row's
+ * largest lose more).  Where x, dlogits or w_g are not finite, so are the results
+ * they reach (NaN in place of some infinities).
  *   ws moe_workspace_size_bwd(s, 1) bytes */
 MOE_API int moe_router_bwd(const moe_bf16* x, const float* w_g, const float* dlogits,
                            const moe_shape* s, float* dw_g, float* dbias, moe_bf16* dx, void* ws,
@@ -567,8 +567,9 @@ enum { MOE_GRAD_FP32 = 0, MOE_GRAD_BF16 = 1 };
  * zeroed once, one call at a time. */
 MOE_API size_t moe_workspace_size_grads(int32_t n);
 
-/* sumsq[0] = the sum of the squares of all elements (fp64 products and sums,
- * in a fixed order).  `grads` is a host array of n entries, read before the
+/* sumsq[0] = the sum of the squares of all elements, in a fixed order: the
+ * squares of up to 8 neighbours are added in fp32 (in fp64 where they leave its
+ * range), those sums in fp64.  `grads` is a host array of n entries, read before the
  * call returns; their `out` is not looked at. */
 MOE_API int moe_grad_sumsq(const moe_grad* grads, int32_t n, double* sumsq, void* ws,
                            void* stream);
