@@ -509,11 +509,18 @@ __global__ void __launch_bounds__(32 * W) k_balance_finish(
   if (b > a) {
     const int blk0 = a / C, blk1 = (b - 1) / C;
     if (e < E) {
-#pragma unroll 4
-      for (int q = blk0 + warp; q <= blk1; q += W) {
-        const size_t slot = (size_t)q + s;
-        p += part.prob[slot * E + e];
-        c += part.count[slot * E + e];
+      for (int q0 = blk0 + warp; q0 <= blk1; q0 += 8 * W) {
+        float v[8];  // 16 loads in flight
+        int m[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const size_t at = ((size_t)q0 + i * W + s) * E + e;
+          const bool in = q0 + i * W <= blk1;
+          v[i] = in ? __ldcg(part.prob + at) : 0.f;
+          m[i] = in ? __ldcg(part.count + at) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p += v[i], c += m[i];
       }
     }
     for (int q = blk0 + (int)threadIdx.x; q <= blk1; q += 32 * W) {
