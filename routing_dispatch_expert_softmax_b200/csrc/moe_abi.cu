@@ -475,7 +475,7 @@ int moe_forward_eplb(const moe_bf16* x, const float* w_g, const float* bias,
 
 size_t moe_workspace_size_bwd(const moe_shape* s, int32_t S) {
   if (!shape_ok(s) || S < 1 || S > kMaxSeqs) return 0;
-  return bwd_layout(*s, S).total;
+  return bwd_bytes(*s, S);
 }
 
 int moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* token_mask,

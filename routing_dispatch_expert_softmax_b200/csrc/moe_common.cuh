@@ -200,11 +200,12 @@ struct BwdLayout {
   int chunk;
   size_t prob, count, z, n, term, zterm;
   // router backward: bf16 planes of dlogits (router_planes), fp16 dlogits [T][cp]
-  // and w_g [d][cp] (cp = E rounded up to 64) with the factors that undo their rows' scaling, column sums of every plane_rows tokens, and
-  // partial weight gradients of the token ranges
+  // and w_g [d][cp] (cp = E rounded up to 64) with the factors that undo their rows'
+  // scaling, column sums of every plane_rows tokens, and (last) partial weight
+  // gradients of the token ranges
   int cp, plane_rows;
   size_t dl_planes, dl_half, w_half, dl_back, w_back, db_part, dw_part;
-  size_t total;
+  size_t rest;  // the bytes of all but dw_part
 };
 
 // How the router's backward lays dL's three bf16 planes out for dW's 128-row MMA
@@ -279,9 +280,10 @@ inline BwdLayout bwd_layout(const moe_shape& s, int S) {
     o = align_up(o + bytes, 256);
     return at;
   };
-  // One sequence of up to 64 tokens: one block.  Else 32 tokens a block (4 for each warp), or the tokens of an average sequence (a
-  // block takes the sequences in its tokens one after the other), until the SMs are
-  // full, with four blocks (three above 256 experts, two above 512) each.
+  // One sequence of up to 64 tokens: one block.  Else 32 tokens a block (4 for each
+  // warp), or the tokens of an average sequence (a block takes the sequences in its
+  // tokens one after the other), until the SMs are full, with four blocks (three above
+  // 256 experts, two above 512) each.
   const long long nblk = E <= 256 ? 592 : E <= 512 ? 444 : 296;
   const long long least = std::min(32LL, std::max(1LL, T / S));
   L.chunk = S == 1 && T <= 64 ? 64 : (int)std::max(least, (T + nblk - 1) / nblk);
@@ -304,11 +306,20 @@ inline BwdLayout bwd_layout(const moe_shape& s, int S) {
   L.dl_back = take(2 * (size_t)T);
   L.w_back = take(2 * (size_t)d);
   L.db_part = take(sizeof(float) * (size_t)((T + L.plane_rows - 1) / L.plane_rows) * E);
-  const long long per = std::min(router_range_blocks(s, false), router_range_blocks(s, true));
-  const long long ranges = ((T + 63) / 64 + per - 1) / per;
-  L.dw_part = take(ranges * pl.parts > 1 ? sizeof(float) * (size_t)ranges * pl.parts * d * E : 0);
-  L.total = std::max(balance, o);
+  L.dw_part = o;
+  L.rest = std::max(balance, o);
   return L;
+}
+
+// The layout's bytes.  Apart from it: the search for the ranges takes the host a
+// microsecond or two, and only their own call needs them.
+inline size_t bwd_bytes(const moe_shape& s, int S) {
+  const BwdLayout L = bwd_layout(s, S);
+  const long long per = std::min(router_range_blocks(s, false), router_range_blocks(s, true));
+  const long long ranges = ((s.T + 63LL) / 64 + per - 1) / per;
+  const int parts = router_planes(s.E, s.T).parts;
+  const size_t part = ranges * parts > 1 ? sizeof(float) * (size_t)ranges * parts * s.d * s.E : 0;
+  return std::max(L.rest, align_up(L.dw_part + part, 256));
 }
 
 // ----------------------------------------------------------------- PTX: misc

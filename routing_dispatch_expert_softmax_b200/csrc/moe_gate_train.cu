@@ -618,7 +618,8 @@ struct GateArgs {
 };
 
 template <int LPR, int NV, bool VEC>
-__global__ void __launch_bounds__(256, RowCfg<LPR, NV, VEC>::kGateBlocks) k_gate_bwd(const GateArgs a) {
+__global__ void __launch_bounds__(256, RowCfg<LPR, NV, VEC>::kGateBlocks)
+    k_gate_bwd(const GateArgs a) {
   using R = RowCfg<LPR, NV, VEC>;
   constexpr int kStep = R::kGroups;
   extern __shared__ float sm[];
@@ -704,8 +705,10 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV, VEC>::kGateBlocks) k_gate
     }
     float dotw = q.w * q.dw;
     if (LPR < 32 && a.dw && in)
-      for (int j = l + LPR; j < a.k; j += LPR)
-        dotw = fmaf(__ldg(a.w + (unsigned)(t * a.k + j)), __ldg(a.dw + (unsigned)(t * a.k + j)), dotw);
+      for (int j = l + LPR; j < a.k; j += LPR) {
+        const unsigned at = t * a.k + j;
+        dotw = fmaf(__ldg(a.w + at), __ldg(a.dw + at), dotw);
+      }
     sum3<LPR>(sum, dot, dotw);
     if (live) {
       // v / sum (f + zc lse - dot / sum)
@@ -954,8 +957,8 @@ cudaError_t launch_gate_bwd(const float* logits, const int* idx, const float* w,
     a.rows_per_warp = (int)rows;
     const long long nw = (s.T + rows - 1) / rows;
     const size_t smem = sizeof(float) * 8 * R::kGroups * R::kCols;
-    return launch_kernel(k_gate_bwd<R::kLpr, R::kNv, R::kVec>, dim3((unsigned)((nw + 7) / 8)), dim3(256),
-                         smem, st, 1, a);
+    return launch_kernel(k_gate_bwd<R::kLpr, R::kNv, R::kVec>, dim3((unsigned)((nw + 7) / 8)),
+                         dim3(256), smem, st, 1, a);
   });
 }
 

@@ -238,7 +238,9 @@ constexpr int kChunk = 2;
 constexpr int kRA = 4, kRB = 4;
 constexpr int kATile = 128 * 64 * 2, kBTile = 256 * 64 * 2;
 constexpr int kStageOut = 2 * 32 * 64;  // per epilogue warp: two times 32 rows x 32 bf16 of dx
-constexpr int router_smem(int rb) { return kRA * kATile + rb * kBTile + 8 * kStageOut + 1024 + 256; }
+constexpr int router_smem(int rb) {
+  return kRA * kATile + rb * kBTile + 8 * kStageOut + 1024 + 256;
+}
 constexpr int kRouterThreads = 320;  // TMA, MMA and eight epilogue warps
 
 // Descriptor of an MN-major operand tile with 128-byte swizzle: blocks of 64
@@ -271,7 +273,8 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, ui
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, const void* src, int c0,
                                              int c1) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(tm)),
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::
+          "l"(reinterpret_cast<uint64_t>(tm)),
       "r"(smem_u32(src)), "r"(c0), "r"(c1)
       : "memory");
 }
@@ -425,7 +428,8 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
       // fp16 A and B (format code 0 in bits [7, 10) and [10, 13)), K-major
       constexpr uint32_t kIdescK = idesc_bf16_f32(128, 256) & ~(1u << 7 | 1u << 10);
       constexpr uint64_t kA = kATile >> 4, kB = kBTile >> 4;  // descriptor units of a slot
-      const uint64_t a_mn = sw128_mnmajor_desc(smem_u32(sa)), b_mn = sw128_mnmajor_desc(smem_u32(sb));
+      const uint64_t a_mn = sw128_mnmajor_desc(smem_u32(sa));
+      const uint64_t b_mn = sw128_mnmajor_desc(smem_u32(sb));
       const uint64_t a_k = sw128_kmajor_desc(smem_u32(sa)), b_k = sw128_kmajor_desc(smem_u32(sb));
       Ring a, b;
       bool ok = true;
@@ -711,7 +715,8 @@ struct RouterSmallArgs {
   __nv_bfloat16* dx;
   int T, d, E, ep, vec_dl, vec_w;
 };
-constexpr int kSmallT = 64, kSmallXPitch = 24, kSmallWarps = 16;  // bf16 of one token of x in shared memory
+constexpr int kSmallT = 64, kSmallWarps = 16;
+constexpr int kSmallXPitch = 24;  // bf16 of one token of x in shared memory
 
 // rows x cols of src into rows of ep words, zeros up to rows_all x cols_all.
 __device__ __forceinline__ void copy_rows(float* dst, const float* __restrict__ src, int rows,
@@ -723,11 +728,13 @@ __device__ __forceinline__ void copy_rows(float* dst, const float* __restrict__ 
     const int n = r < rows ? cols : 0;
     if (vec) {
       for (int c = 4 * lane; c < n; c += 128)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + c)), "l"(from + c)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + c)),
+                     "l"(from + c)
                      : "memory");
     } else {
       for (int c = lane; c < n; c += 32)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to + c)), "l"(from + c)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to + c)),
+                     "l"(from + c)
                      : "memory");
     }
     for (int c = n + lane; c < cols_all; c += 32) to[c] = 0.f;
@@ -763,10 +770,11 @@ __device__ __forceinline__ uint32_t pair_of(__nv_bfloat16 lo, __nv_bfloat16 hi) 
 __global__ void __launch_bounds__(32 * kSmallWarps) k_router_bwd_small(const RouterSmallArgs a) {
   extern __shared__ __align__(16) float sm[];
   const int T16 = (a.T + 15) / 16 * 16, E8 = (a.E + 7) / 8 * 8;
-  float* sdl = sm;                                                   // [T16][ep]
-  float* sw = sdl + (size_t)T16 * a.ep;                              // [16][ep]
-  float* meet = sw + 16 * a.ep;                                      // [8 warps][16][16]
-  __nv_bfloat16* sx = reinterpret_cast<__nv_bfloat16*>(meet + 256 * kSmallWarps);  // [T16][kSmallXPitch]
+  float* sdl = sm;                       // [T16][ep]
+  float* sw = sdl + (size_t)T16 * a.ep;  // [16][ep]
+  float* meet = sw + 16 * a.ep;          // [warp][16][16]
+  __nv_bfloat16* sx =                    // [T16][kSmallXPitch]
+      reinterpret_cast<__nv_bfloat16*>(meet + 256 * kSmallWarps);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t4 = lane & 3;  // a fragment's row or column, and place in it
   pdl_trigger();
@@ -862,7 +870,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps) k_router_bwd_small(const Rou
     }
   }
   if (a.db)  // each block some experts
-    for (int e = blockIdx.x * 32 * kSmallWarps + threadIdx.x; e < a.E; e += gridDim.x * 32 * kSmallWarps) {
+    for (int e = blockIdx.x * blockDim.x + threadIdx.x; e < a.E; e += gridDim.x * blockDim.x) {
       float s = 0.f;
 #pragma unroll 8
       for (int r = 0; r < a.T; ++r) s += sdl[r * a.ep + e];
@@ -888,7 +896,8 @@ bool router_small(const moe_shape& s, int sms) {
          router_small_smem(s) <= kSmallSmem;
 }
 
-// 16-bit tensor map of up to 4 dimensions, innermost first; strides in bytes of dimensions 1 and up.
+// 16-bit tensor map of up to 4 dimensions, innermost first; strides in bytes of
+// dimensions 1 and up.
 bool make_map(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
               const uint64_t* strides, const uint32_t* box,
               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
@@ -899,7 +908,8 @@ bool make_map(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
   for (int i = 0; i < rank; ++i) d[i] = dims[i], b[i] = box[i];
   for (int i = 0; i + 1 < rank; ++i) s[i] = strides[i];
   return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, s, b, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
 
@@ -950,8 +960,9 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
   const int sum_rows = (T + L.plane_rows - 1) / L.plane_rows;
   // one block's column sums are db itself
   const PlanesArgs pd{dl, dw ? dlp : nullptr, dx ? dlh : nullptr, dl_back,
-                      !db ? nullptr : sum_rows == 1 ? db : sums, T, prow, apart ? (long long)T * pl.width : pl.width, E, cp, pl.width,
-                      !apart, L.plane_rows, sum_rows, vec(dl)};
+                      !db ? nullptr : sum_rows == 1 ? db : sums, T, prow,
+                      apart ? (long long)T * pl.width : pl.width, E, cp, pl.width, !apart,
+                      L.plane_rows, sum_rows, vec(dl)};
   const PlanesArgs pw{w_g, nullptr, wh, w_back, nullptr, d, 0, 0, E, cp, 0, 0, 32,
                       dx ? (d + 31) / 32 : 0, vec(w_g)};
   const auto planes = [&](auto kern, int lanes) {
@@ -984,8 +995,8 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
     // `more` dx items; a level n of dx items for the heavy ones gives the others
     // n + more.
     const int heavy = a.dw_items % grid, light = grid - heavy;
-    const double more =
-        (std::min(kper, kblocks) * router_dw_block_us(pl.sets) + kRouterItemUs) / router_dx_tile_us(E);
+    const double item_us = std::min(kper, kblocks) * router_dw_block_us(pl.sets) + kRouterItemUs;
+    const double more = item_us / router_dx_tile_us(E);
     const double level = std::max(0.0, (a.dx_items - light * more) / grid);
     a.light_dx = heavy == 0 ? a.dx_items
                             : (int)std::min<double>(a.dx_items, light * (level + more) + 0.5);
@@ -1006,8 +1017,8 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
                !make_map(&mdx, dx, 2, od, os, ob, CU_TENSOR_MAP_SWIZZLE_64B)))
       return cudaErrorInvalidValue;
     if ((e = allow_smem(k_router_gemm, router_smem(kRB), gemm_ready)) != cudaSuccess) return e;
-    e = launch_kernel(k_router_gemm, dim3(grid), dim3(kRouterThreads), router_smem(a.rb), st, 1, mx, mn,
-                      mk, mw, mdx, a);
+    e = launch_kernel(k_router_gemm, dim3(grid), dim3(kRouterThreads), router_smem(a.rb), st, 1,
+                      mx, mn, mk, mw, mdx, a);
     if (e != cudaSuccess) return e;
   }
   const long long n = (long long)d * E;
