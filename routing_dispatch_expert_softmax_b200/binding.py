@@ -509,14 +509,16 @@ class _Operands:
     def ptr(self, t, dtype, shape, name, optional=False):
         if t is None and optional:
             return None
-        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous()
-                and (shape is None or t.shape == shape)):
-            index = t.get_device()
-            if index == self.index and index >= 0:
-                return t.data_ptr()
-            if self.index is None and index >= 0:
-                self.index = index
-                return t.data_ptr()
+        try:
+            if t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape):
+                index = t.get_device()
+                if index == self.index and index >= 0:
+                    return t.data_ptr()
+                if self.index is None and index >= 0:
+                    self.index = index
+                    return t.data_ptr()
+        except AttributeError:  # not a tensor
+            pass
         self._refuse(t, dtype, shape, name)
 
     def _refuse(self, t, dtype, shape, name):
@@ -581,9 +583,10 @@ def workspace_bwd(shape: MoEShape, S: int = 1, device="cuda") -> torch.Tensor:
 def _seq_count(where, seq_offsets) -> int:
     if seq_offsets is None:
         return 1
-    if not isinstance(seq_offsets, torch.Tensor) or seq_offsets.dim() != 1 or len(seq_offsets) < 2:
+    if (not isinstance(seq_offsets, torch.Tensor) or seq_offsets.dim() != 1
+            or seq_offsets.numel() < 2):
         raise ValueError(f"{where}: seq_offsets must be a tensor of S + 1 >= 2 offsets")
-    return len(seq_offsets) - 1
+    return seq_offsets.numel() - 1
 
 
 def moe_balance_loss(logits, idx, loss, counts, tokens, shape: MoEShape, ws, balance_coef=1e-2,
