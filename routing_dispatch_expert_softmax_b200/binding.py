@@ -1,7 +1,7 @@
 """Thin ctypes binding of ``libmoe_b200.so`` (the C ABI in ``include/moe.h``).
 
-Argument marshalling only: every step of the layer runs in the library's CUDA
-kernels.  Tensors are torch CUDA tensors (PyTorch supplies device memory and
+Argument marshalling only (the checks of the calls that train the gate natively, in
+``_operands.so``): every step of the layer runs in the library's CUDA kernels.  Tensors are torch CUDA tensors (PyTorch supplies device memory and
 streams; the layer calls' y and moe_copy's operands may also be pinned host
 tensors); the functions keep the C names and raise :class:`MoEError` on a
 non-zero status.  There is no fallback: if the library is missing or the
@@ -16,6 +16,11 @@ import os
 from typing import Optional
 
 import torch
+
+try:
+    from . import _operands as _native  # csrc/operands.cpp
+except ImportError as err:  # not built, or for another torch: load_library says so
+    _native, _native_error = None, err
 
 LIB_NAME = "libmoe_b200.so"
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), LIB_NAME)
@@ -79,6 +84,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         raise RuntimeError(
             f"{LIB_NAME} is not built (expected at {path}); run "
             "`python -m routing_dispatch_expert_softmax_b200.build`")
+    if _native is None:
+        raise RuntimeError("_operands.so is not built for this Python and torch; run "
+                           "`python -m routing_dispatch_expert_softmax_b200.build`"
+                           ) from _native_error
+    if _native.TORCH != str(torch.__version__).split("+")[0]:
+        raise RuntimeError(f"_operands.so is built for torch {_native.TORCH}; run "
+                           "`python -m routing_dispatch_expert_softmax_b200.build`")
     lib = ctypes.CDLL(path)
     lib.moe_error_string.restype = ctypes.c_char_p
     lib.moe_error_string.argtypes = [ctypes.c_int]
@@ -495,31 +507,18 @@ def moe_forward_fp8_staged(x, w_g, bias, w13, w13_scale, w2, w2_scale, y, shape:
 
 
 # ------------------------------------------------------- training the gate
-class _Operands:
-    """The tensors of one call: each is checked (CUDA, dtype, shape,
-    contiguity, the call's one device) and gives its address; ``launch`` runs
-    the call on that device and the stream asked for (default: the device's
-    current one)."""
+class _NotBuilt:
+    def __init__(self, where):
+        load_library()  # raises
 
-    __slots__ = ("where", "index")
 
-    def __init__(self, where: str):
-        self.where, self.index = where, None
+class _Operands(_native.Operands if _native else _NotBuilt):
+    """The tensors of one call: ``ptr(t, dtype, shape, name, optional)`` checks
+    one (CUDA, dtype, shape, contiguity, the call's one device) and gives its
+    address; ``launch`` runs the call on that device and the stream asked for
+    (default: the device's current one)."""
 
-    def ptr(self, t, dtype, shape, name, optional=False):
-        if t is None and optional:
-            return None
-        try:
-            if t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape):
-                index = t.get_device()
-                if index == self.index and index >= 0:
-                    return t.data_ptr()
-                if self.index is None and index >= 0:
-                    self.index = index
-                    return t.data_ptr()
-        except AttributeError:  # not a tensor
-            pass
-        self._refuse(t, dtype, shape, name)
+    __slots__ = ()
 
     def _refuse(self, t, dtype, shape, name):
         if t is None:
@@ -690,8 +689,9 @@ class GradList:
         self.n = len(self.grads)
         self._entries = (MoEGrad * self.n)()
         self._seen = None
+        lib = load_library()
         self._refresh()
-        need = int(load_library().moe_workspace_size_grads(self.n))
+        need = int(lib.moe_workspace_size_grads(self.n))
         if need == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "moe_workspace_size_grads")
         self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
@@ -699,9 +699,7 @@ class GradList:
     def _refresh(self):
         """Checks the tensors and fills the entries, unless no address has
         changed since the last time."""
-        seen = list(map(torch.Tensor.data_ptr, self.grads))
-        if self.outs is not self.grads:
-            seen += map(torch.Tensor.data_ptr, self.outs)
+        seen = _native.addresses(self.grads, None if self.outs is self.grads else self.outs)
         if seen == self._seen:
             return
         o = _Operands("GradList")

@@ -1,8 +1,9 @@
-"""Builds the in-tree C-ABI shared library ``libmoe_b200.so`` for sm_100a.
+"""Builds the in-tree C-ABI shared library ``libmoe_b200.so`` for sm_100a, and
+``_operands.so``, the binding's native tensor checks.
 
 Run as ``python -m routing_dispatch_expert_softmax_b200.build``.  nvcc
-cross-compiles without a GPU; the library lands next to this file so it
-travels with the source tree.
+cross-compiles without a GPU; the libraries land next to this file so they
+travel with the source tree.
 """
 
 from __future__ import annotations
@@ -12,11 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libmoe_b200.so")
+OPERANDS_SRC = os.path.join(CSRC, "operands.cpp")
+OPERANDS_OUT = os.path.join(HERE, "_operands.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["moe_abi.cu", "moe_routing.cu", "moe_gemm_sm100.cu", "moe_noalloc.cu", "moe_w8a8.cu",
@@ -42,9 +46,34 @@ def _run(cmd):
     return p.stdout + p.stderr
 
 
+def build_operands(force: bool = False) -> str:
+    """Compile the Python extension of the binding's checks against torch's headers."""
+    import torch
+    # rebuilt for another torch: its tensors' layout belongs to one version
+    stamp = os.path.join(BUILD_DIR, "operands.torch")
+    built_for = open(stamp).read() if os.path.exists(stamp) else ""
+    if (not force and os.path.exists(OPERANDS_OUT) and built_for == str(torch.__version__)
+            and os.path.getmtime(OPERANDS_OUT) > os.path.getmtime(OPERANDS_SRC)):
+        return OPERANDS_OUT
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    tmp = OPERANDS_OUT + ".tmp"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+          *(a for i in inc for a in ("-isystem", i)), OPERANDS_SRC, "-o", tmp,
+          "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
+    os.replace(tmp, OPERANDS_OUT)
+    with open(stamp, "w") as f:
+        f.write(str(torch.__version__))
+    return OPERANDS_OUT
+
+
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
-    """Compile every .cu for sm_100a and link the shared library."""
+    """Compile every .cu for sm_100a and link the shared library; the extension beside it."""
     os.makedirs(BUILD_DIR, exist_ok=True)
+    build_operands(force)
     nvcc = _nvcc()
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     deps = srcs + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")]

@@ -4,6 +4,7 @@ Python binding.  Nothing here reaches a kernel."""
 
 import ctypes
 import math
+import sys
 
 import numpy as np
 import pytest
@@ -241,3 +242,55 @@ def test_binding_refuses(lib):
         moe.GradList([cpu], [cpu[:3]])
     with pytest.raises(ValueError, match="CUDA tensor"):
         moe.GradList([cpu])
+
+
+def test_operand_checks(lib):
+    class Seen(B._native.Operands):
+        def _refuse(self, *a):
+            raise KeyError(a)
+
+    o = Seen("call")
+    assert o.where == "call" and o.index is None
+    t = torch.zeros(3, 4)
+    assert o.ptr(None, torch.float32, (3, 4), "t", True) is None
+    for a in ((None, torch.float32, (3, 4), "t"), (None, torch.float32, (3, 4), "t", False),
+              (t, torch.float32, (3, 4), "t"),  # no CUDA tensor
+              (t, torch.float32, ("x", 4), "t"), (t, "float32", None, "t"), (3, torch.float32, None, "t"),
+              (torch.zeros(2, device="meta"), torch.float32, None, "t")):
+        with pytest.raises(KeyError) as e:
+            o.ptr(*a)
+        assert e.value.args[0] == a[:4] and o.index is None
+    o.index = 3
+    assert o.index == 3
+    with pytest.raises(TypeError):
+        o.index = "cuda"
+    with pytest.raises(TypeError):
+        o.ptr(t)
+    with pytest.raises(TypeError):
+        B._native.Operands("call", 1)
+
+    class Silent(B._native.Operands):
+        def _refuse(self, *a):
+            pass
+
+    with pytest.raises(RuntimeError, match="without a reason"):
+        Silent("call").ptr(t, torch.float32, None, "t")
+
+
+def test_addresses(lib):
+    ts = [torch.zeros(i + 1) for i in range(5)]
+    want = [t.data_ptr() for t in ts]
+    got = np.frombuffer(B._native.addresses(ts, None), dtype=np.uint64).tolist()
+    assert got == want
+    got = np.frombuffer(B._native.addresses(ts[:2], ts[3:]), dtype=np.uint64).tolist()
+    assert got == want[:2] + want[3:]
+    assert B._native.addresses([], None) == b""
+    for a in (((), None), ([3], None), ([], [None]), ([], 3)):
+        with pytest.raises(TypeError):
+            B._native.addresses(*a)
+    # nothing is kept: references do not grow
+    before = sys.getrefcount(ts[0])
+    for _ in range(100):
+        B._native.addresses(ts, ts)
+    after = sys.getrefcount(ts[0])
+    assert after == before
