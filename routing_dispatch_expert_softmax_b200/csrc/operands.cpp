@@ -24,7 +24,7 @@ namespace {
 struct Operands {
   PyObject_HEAD
   PyObject* where;
-  int index;  // -1: none yet
+  int device;  // the device's index + 1; 0: none yet
 };
 
 int operands_init(Operands* self, PyObject* args, PyObject* kw) {
@@ -36,7 +36,7 @@ int operands_init(Operands* self, PyObject* args, PyObject* kw) {
   if (!PyArg_ParseTuple(args, "O:Operands", &where)) return -1;
   Py_INCREF(where);
   Py_XSETREF(self->where, where);
-  self->index = -1;
+  self->device = 0;
   return 0;
 }
 
@@ -78,9 +78,9 @@ PyObject* operands_ptr(Operands* self, PyObject* const* args, Py_ssize_t n) {
     if (THPVariable_Check(t)) {
       const at::Tensor& v = THPVariable_Unpack(t);
       if (fits(v, args[1], args[2])) {
-        const int index = static_cast<int>(v.get_device());
-        if (index >= 0 && (self->index < 0 || self->index == index)) {
-          self->index = index;
+        const int device = static_cast<int>(v.get_device()) + 1;
+        if (device > 0 && (self->device == 0 || self->device == device)) {
+          self->device = device;
           return PyLong_FromVoidPtr(v.data_ptr());
         }
       }
@@ -100,14 +100,18 @@ PyObject* operands_ptr(Operands* self, PyObject* const* args, Py_ssize_t n) {
 }
 
 PyObject* get_index(Operands* self, void*) {
-  if (self->index < 0) Py_RETURN_NONE;
-  return PyLong_FromLong(self->index);
+  if (self->device == 0) Py_RETURN_NONE;
+  return PyLong_FromLong(self->device - 1);
 }
 
 int set_index(Operands* self, PyObject* value, void*) {
   const long i = value ? PyLong_AsLong(value) : -1;
   if (i == -1 && PyErr_Occurred()) return -1;
-  self->index = static_cast<int>(i);
+  if (i < 0 || i >= 1024) {
+    PyErr_SetString(PyExc_ValueError, "index of a CUDA device expected");
+    return -1;
+  }
+  self->device = static_cast<int>(i) + 1;
   return 0;
 }
 

@@ -264,6 +264,8 @@ def test_operand_checks(lib):
     assert o.index == 3
     with pytest.raises(TypeError):
         o.index = "cuda"
+    with pytest.raises(ValueError):
+        o.index = -1
     with pytest.raises(TypeError):
         o.ptr(t)
     with pytest.raises(TypeError):
