@@ -704,8 +704,8 @@ __global__ void __launch_bounds__(256) k_router_sum(const float* __restrict__ pa
 //   dx: 16 tokens x 8 columns a tile, K = experts, both rounded to tf32 (2^-11 of each
 //       value, as fp16 keeps in the large path; no scaling, tf32 has fp32's range).
 // Rows lie ep = 4 (mod 32) words apart: the 8 x 4 lanes of a fragment hit 32 banks.
-// Every block reads all of dL from L2, which is most of the time (64 x 2048 x 128: 7.5
-// us, 4.4 with 16 tokens; 8 warps a block took 10.8, 16 as here hide more of it).
+// Every block reads all of dL from L2, which is most of the time (64 x 2048 x 128: 6.8
+// us, 3.7 with 16 tokens; 8 warps a block in place of 16 took 3 us more).
 struct RouterSmallArgs {
   const __nv_bfloat16* x;
   const float* w;
@@ -767,9 +767,13 @@ __device__ __forceinline__ uint32_t pair_of(__nv_bfloat16 lo, __nv_bfloat16 hi) 
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__global__ void __launch_bounds__(32 * kSmallWarps) k_router_bwd_small(const RouterSmallArgs a) {
+// KS: 16 tokens each, so that the steps of a tile are unrolled without a branch
+// (64 x 2048 x 128: 6.8 us; with one that leaves the loop early 7.6).
+template <int KS>
+__global__ void __launch_bounds__(32 * kSmallWarps, 2) k_router_bwd_small(const RouterSmallArgs a) {
   extern __shared__ __align__(16) float sm[];
-  const int T16 = (a.T + 15) / 16 * 16, E8 = (a.E + 7) / 8 * 8;
+  constexpr int T16 = 16 * KS;
+  const int E8 = (a.E + 7) / 8 * 8;
   float* sdl = sm;                       // [T16][ep]
   float* sw = sdl + (size_t)T16 * a.ep;  // [16][ep]
   float* meet = sw + 16 * a.ep;          // [warp][16][16]
@@ -793,10 +797,9 @@ __global__ void __launch_bounds__(32 * kSmallWarps) k_router_bwd_small(const Rou
   __syncthreads();
 
   if (a.dw) {
-    uint32_t xa[kSmallT / 16][4];
+    uint32_t xa[KS][4];
 #pragma unroll
-    for (int ks = 0; ks < kSmallT / 16; ++ks) {
-      if (16 * ks >= T16) break;
+    for (int ks = 0; ks < KS; ++ks) {
       const __nv_bfloat16* p = sx + (16 * ks + 2 * t4) * kSmallXPitch + g;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // rows g, g + 8; tokens 2 t4, + 8
@@ -808,8 +811,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps) k_router_bwd_small(const Rou
     for (int nt = warp; nt < E8 / 8; nt += kSmallWarps) {
       float c[4] = {}, cm[4] = {}, cl[4] = {};
 #pragma unroll
-      for (int ks = 0; ks < kSmallT / 16; ++ks) {
-        if (16 * ks >= T16) break;
+      for (int ks = 0; ks < KS; ++ks) {
         const float* p = sdl + (16 * ks + 2 * t4) * a.ep + 8 * nt + g;
         const Split3 v0 = split3(p[0]), v1 = split3(p[a.ep]);
         const Split3 v2 = split3(p[8 * a.ep]), v3 = split3(p[9 * a.ep]);
@@ -834,7 +836,8 @@ __global__ void __launch_bounds__(32 * kSmallWarps) k_router_bwd_small(const Rou
   }
   if (a.dx) {
     // a warp takes 16 tokens, and with fewer than 8 such tiles a part of the experts
-    const int tiles = T16 / 16, parts = kSmallWarps / tiles, mt = warp % tiles, part = warp / tiles;
+    constexpr int tiles = KS, parts = kSmallWarps / tiles;
+    const int mt = warp % tiles, part = warp / tiles;
     float c[2][4] = {};
     if (part < parts) {
       const int n8 = E8 / 8;
@@ -916,7 +919,7 @@ bool make_map(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
 // Raises a kernel's dynamic shared memory limit once for each device (the attribute
 // belongs to the device's copy of the kernel); `ready` has a bit for each.
 typedef std::atomic<uint64_t> DeviceBits[2];
-DeviceBits gemm_ready, small_ready;
+DeviceBits gemm_ready, small_ready[4];
 template <class K>
 cudaError_t allow_smem(K kern, int bytes, DeviceBits& ready) {
   int dev = 0;
@@ -941,11 +944,17 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
   };
   const bool products = dw || dx;
   if (products && router_small(s, sms)) {
-    cudaError_t e = allow_smem(k_router_bwd_small, kSmallSmem, small_ready);
-    if (e != cudaSuccess) return e;
     const RouterSmallArgs a{x, w_g, dl, dw, db, dx, T, d, E, router_small_ep(E), vec(dl), vec(w_g)};
-    return launch_kernel(k_router_bwd_small, dim3(d / 16), dim3(32 * kSmallWarps),
-                         router_small_smem(s), st, 1, a);
+    const auto go = [&](auto kern, DeviceBits& ready) {
+      const cudaError_t e = allow_smem(kern, kSmallSmem, ready);
+      if (e != cudaSuccess) return e;
+      return launch_kernel(kern, dim3(d / 16), dim3(32 * kSmallWarps), router_small_smem(s), st, 1,
+                           a);
+    };
+    return T <= 16   ? go(k_router_bwd_small<1>, small_ready[0])
+           : T <= 32 ? go(k_router_bwd_small<2>, small_ready[1])
+           : T <= 48 ? go(k_router_bwd_small<3>, small_ready[2])
+                     : go(k_router_bwd_small<4>, small_ready[3]);
   }
   __nv_bfloat16* dlp = reinterpret_cast<__nv_bfloat16*>(ws + L.dl_planes);
   __half* dlh = reinterpret_cast<__half*>(ws + L.dl_half);
