@@ -3,8 +3,7 @@
 //   dx[t,i] = sum_e dL[t,e] W[i,e]
 // on the sm_100a tensor cores.  dL and W are fp32; the tensor cores take 16-bit
 // operands.  A first kernel prepares them:
-//   dW: dL splits into three bf16 planes, hi = bf16(v), mid = bf16(v - hi),
-//       lo = bf16(v - hi - mid), hi + mid + lo = v to more than 24 bits.  x is
+//   dW: dL splits into three bf16 planes of 8 bits each, hi + mid + lo = v.  x is
 //       bf16, so the three products are exact and dW is as good as an fp32
 //       product's;
 //   dx: dx is rounded to bf16 (2^-8), so dL and W are rounded to fp16, which
@@ -32,19 +31,25 @@ namespace moe {
 namespace {
 
 // ============================================================== planes
+// Two values as pairs of bf16 (a in the low half): hi has the upper 8 bits of the
+// mantissa as they stand, the rest v - hi is exact, mid has its upper 8 bits and lo the
+// last 8: nothing is rounded.  11 instructions a pair; rounding each part to nearest,
+// with its care for overflow, took four times as many (few tokens: 64 x
+// 2048 x 128 6.0 us in place of 6.8; the three kernels 0.4 less).  inf leaves
+// NaN in the rest, and a NaN as well.
 struct Split3 {
-  __nv_bfloat16 hi, mid, lo;
+  uint32_t hi, mid, lo;
 };
-
-// inf and NaN go to hi alone, so that a product shows them as an fp32 one would.
-__device__ __forceinline__ Split3 split3(float v) {
+__device__ __forceinline__ Split3 split3(float a, float b) {
+  const auto upper = [](float v) { return __uint_as_float(__float_as_uint(v) & 0xffff0000u); };
+  const auto halves = [](float x, float y) {
+    return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+  };
   Split3 s;
-  s.hi = __float2bfloat16_rn(v);
-  if (__hisinf(s.hi)) s.hi = __float2bfloat16_rz(v);  // the largest fp32 values round to inf
-  float r = v - __bfloat162float(s.hi);
-  if (!(fabsf(v) <= 3.402823466e38f)) r = 0.f;
-  s.mid = __float2bfloat16_rn(r);
-  s.lo = __float2bfloat16_rn(r - __bfloat162float(s.mid));
+  s.hi = halves(a, b);
+  a -= upper(a), b -= upper(b);
+  s.mid = halves(a, b);
+  s.lo = halves(a - upper(a), b - upper(b));
   return s;
 }
 
@@ -125,13 +130,8 @@ __device__ void planes_block(const PlanesArgs& p, int block, float* red) {
         uint32_t w[3][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const Split3 a = split3(v[n][2 * i]), b = split3(v[n][2 * i + 1]);
-          const __nv_bfloat162 h = __halves2bfloat162(a.hi, b.hi);
-          const __nv_bfloat162 m = __halves2bfloat162(a.mid, b.mid);
-          const __nv_bfloat162 q = __halves2bfloat162(a.lo, b.lo);
-          w[0][i] = *reinterpret_cast<const uint32_t*>(&h);
-          w[1][i] = *reinterpret_cast<const uint32_t*>(&m);
-          w[2][i] = *reinterpret_cast<const uint32_t*>(&q);
+          const Split3 q = split3(v[n][2 * i], v[n][2 * i + 1]);
+          w[0][i] = q.hi, w[1][i] = q.mid, w[2][i] = q.lo;
         }
 #pragma unroll
         for (int q = 0; q < 3; ++q)
@@ -704,8 +704,8 @@ __global__ void __launch_bounds__(256) k_router_sum(const float* __restrict__ pa
 //   dx: 16 tokens x 8 columns a tile, K = experts, both rounded to tf32 (2^-11 of each
 //       value, as fp16 keeps in the large path; no scaling, tf32 has fp32's range).
 // Rows lie ep = 4 (mod 32) words apart: the 8 x 4 lanes of a fragment hit 32 banks.
-// Every block reads all of dL from L2, which is most of the time (64 x 2048 x 128: 6.8
-// us, 3.7 with 16 tokens; 8 warps a block in place of 16 took 3 us more).
+// Every block reads all of dL from L2, which is most of the time (64 x 2048 x 128: 6.0
+// us, 3.5 with 16 tokens; 8 warps a block in place of 16 took 3 us more).
 struct RouterSmallArgs {
   const __nv_bfloat16* x;
   const float* w;
@@ -768,7 +768,7 @@ __device__ __forceinline__ uint32_t pair_of(__nv_bfloat16 lo, __nv_bfloat16 hi) 
 }
 
 // KS: 16 tokens each, so that the steps of a tile are unrolled without a branch
-// (64 x 2048 x 128: 6.8 us; with one that leaves the loop early 7.6).
+// (64 x 2048 x 128: 6.8 us with them, 7.6 with one that leaves the loop early).
 template <int KS>
 __global__ void __launch_bounds__(32 * kSmallWarps, 2) k_router_bwd_small(const RouterSmallArgs a) {
   extern __shared__ __align__(16) float sm[];
@@ -813,11 +813,10 @@ __global__ void __launch_bounds__(32 * kSmallWarps, 2) k_router_bwd_small(const 
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         const float* p = sdl + (16 * ks + 2 * t4) * a.ep + 8 * nt + g;
-        const Split3 v0 = split3(p[0]), v1 = split3(p[a.ep]);
-        const Split3 v2 = split3(p[8 * a.ep]), v3 = split3(p[9 * a.ep]);
-        mma_bf16(cl, xa[ks], pair_of(v0.lo, v1.lo), pair_of(v2.lo, v3.lo));
-        mma_bf16(cm, xa[ks], pair_of(v0.mid, v1.mid), pair_of(v2.mid, v3.mid));
-        mma_bf16(c, xa[ks], pair_of(v0.hi, v1.hi), pair_of(v2.hi, v3.hi));
+        const Split3 u = split3(p[0], p[a.ep]), v = split3(p[8 * a.ep], p[9 * a.ep]);
+        mma_bf16(cl, xa[ks], u.lo, v.lo);
+        mma_bf16(cm, xa[ks], u.mid, v.mid);
+        mma_bf16(c, xa[ks], u.hi, v.hi);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) c[i] += cm[i] + cl[i];
