@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(256) k_router_sum(const float* __restrict__ pa
 }
 
 // ============================================================== few tokens
-// Up to 64 tokens the products are small (64 x 2048 x 128: 134 MFLOP) and the time is
+// Up to 192 tokens the products are small (64 x 2048 x 128: 134 MFLOP) and the time is
 // launches, loads and stores, so all of it is one kernel and warp-wide MMAs on
 // fragments made in registers: the tcgen05 tiles want their operands laid out by a
 // kernel before.  A block takes 16 columns of d, with dL [T][E], its W [16][E] and its
@@ -715,7 +715,7 @@ struct RouterSmallArgs {
   __nv_bfloat16* dx;
   int T, d, E, ep, vec_dl, vec_w;
 };
-constexpr int kSmallT = 64, kSmallWarps = 16;
+constexpr int kSmallT = 192, kSmallWarps = 16;
 constexpr int kSmallXPitch = 24;  // bf16 of one token of x in shared memory
 
 // rows x cols of src into rows of ep words, zeros up to rows_all x cols_all.
@@ -770,7 +770,8 @@ __device__ __forceinline__ uint32_t pair_of(__nv_bfloat16 lo, __nv_bfloat16 hi) 
 // KS: 16 tokens each, so that the steps of a tile are unrolled without a branch
 // (64 x 2048 x 128: 6.8 us with them, 7.6 with one that leaves the loop early).
 template <int KS>
-__global__ void __launch_bounds__(32 * kSmallWarps, 2) k_router_bwd_small(const RouterSmallArgs a) {
+__global__ void __launch_bounds__(32 * kSmallWarps, KS <= 4 ? 2 : 1)
+    k_router_bwd_small(const RouterSmallArgs a) {
   extern __shared__ __align__(16) float sm[];
   constexpr int T16 = 16 * KS;
   const int E8 = (a.E + 7) / 8 * 8;
@@ -880,22 +881,29 @@ __global__ void __launch_bounds__(32 * kSmallWarps, 2) k_router_bwd_small(const 
     }
 }
 
-constexpr int kSmallSmem = 113 * 1024;  // two blocks an SM
+constexpr int kSmallSmem = 220 * 1024, kSmallSmem2 = 113 * 1024;  // one, two blocks an SM
 
+// The KS that takes T tokens.
+int router_small_steps(int T) {
+  const int ks = (T + 15) / 16;
+  return ks <= 4 ? ks : ks <= 6 ? 6 : ks <= 8 ? 8 : 12;
+}
 int router_small_ep(int E) { return ((E + 7) / 8 * 8 + 27) / 32 * 32 + 4; }
 size_t router_small_smem(const moe_shape& s) {
-  const size_t T16 = (s.T + 15) / 16 * 16;
+  const size_t T16 = 16 * router_small_steps(s.T);
   return sizeof(float) * ((T16 + 16) * router_small_ep(s.E) + 256 * kSmallWarps) +
          2 * T16 * kSmallXPitch;
 }
-// Where the blocks of 16 columns fit the GPU at once: E = 8 to 256, d = 512 to 4096, 4
-// to 64 tokens took 3.1 to 12.3 us where the three kernels took 7.6 to 14.2, less in
-// each of 48.  In a second wave (d = 7168) each block loads dL again: 4 and 16 tokens
-// still won (5.6 to 10.3 against 8.1 to 12.7), 32 lost at two of four E, 64 at all (20.9
-// against 15.3 with 256 experts).
+// Where the blocks of 16 columns fit the GPU at once (two an SM up to 64 tokens): E = 8
+// to 256, d = 512 to 4096, 16 to 64 tokens took 2.7 to 10.3 us where the three kernels
+// took 7.6 to 13.2, d = 512 and 2048, 96 to 192 tokens 4.8 to 10.3 in place of 10.2 to
+// 13.8, less in each.  In a second wave each block loads dL again: up to 32 tokens still
+// won (d = 7168: 4.9 to 10.6 against 8.1 to 12.4), 64 did at no E but 8 (16.0 against
+// 14.2 with 256 experts).
 bool router_small(const moe_shape& s, int sms) {
-  return s.T <= kSmallT && s.d / 16 <= (s.T <= 16 ? 4 : 2) * sms &&
-         router_small_smem(s) <= kSmallSmem;
+  if (s.T > kSmallT || router_small_smem(s) > kSmallSmem) return false;
+  const int resident = s.T <= 64 && router_small_smem(s) <= kSmallSmem2 ? 2 * sms : sms;
+  return s.d / 16 <= (s.T <= 32 ? 2 * resident : resident);
 }
 
 // 16-bit tensor map of up to 4 dimensions, innermost first; strides in bytes of
@@ -918,7 +926,7 @@ bool make_map(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
 // Raises a kernel's dynamic shared memory limit once for each device (the attribute
 // belongs to the device's copy of the kernel); `ready` has a bit for each.
 typedef std::atomic<uint64_t> DeviceBits[2];
-DeviceBits gemm_ready, small_ready[4];
+DeviceBits gemm_ready, small_ready[7];
 template <class K>
 cudaError_t allow_smem(K kern, int bytes, DeviceBits& ready) {
   int dev = 0;
@@ -950,10 +958,15 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
       return launch_kernel(kern, dim3(d / 16), dim3(32 * kSmallWarps), router_small_smem(s), st, 1,
                            a);
     };
-    return T <= 16   ? go(k_router_bwd_small<1>, small_ready[0])
-           : T <= 32 ? go(k_router_bwd_small<2>, small_ready[1])
-           : T <= 48 ? go(k_router_bwd_small<3>, small_ready[2])
-                     : go(k_router_bwd_small<4>, small_ready[3]);
+    switch (router_small_steps(T)) {
+      case 1: return go(k_router_bwd_small<1>, small_ready[0]);
+      case 2: return go(k_router_bwd_small<2>, small_ready[1]);
+      case 3: return go(k_router_bwd_small<3>, small_ready[2]);
+      case 4: return go(k_router_bwd_small<4>, small_ready[3]);
+      case 6: return go(k_router_bwd_small<6>, small_ready[4]);
+      case 8: return go(k_router_bwd_small<8>, small_ready[5]);
+      default: return go(k_router_bwd_small<12>, small_ready[6]);
+    }
   }
   __nv_bfloat16* dlp = reinterpret_cast<__nv_bfloat16*>(ws + L.dl_planes);
   __half* dlh = reinterpret_cast<__half*>(ws + L.dl_half);

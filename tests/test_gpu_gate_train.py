@@ -457,15 +457,15 @@ def test_router_bwd_tiny_and_huge_gradients():
     check_router(100, 64, 16, scale=1e30)
 
 
-@pytest.mark.parametrize("T", [1, 7, 15, 16, 17, 32, 33, 63, 64, 65])
+@pytest.mark.parametrize("T", [1, 7, 15, 16, 17, 32, 33, 63, 64, 65, 96, 97, 128, 129, 192, 193])
 @pytest.mark.parametrize("d,E", [(64, 1), (64, 3), (128, 8), (448, 60), (1088, 130), (4672, 36), (4736, 9), (4800, 16),
-                                 (64, 255), (128, 260), (64, 640), (9472, 5), (9536, 5)])
+                                 (64, 255), (128, 260), (64, 640), (9472, 5), (9536, 5), (2368, 8), (2432, 8)])
 def test_router_bwd_few_tokens(T, d, E):
     check_router(T, d, E)
 
 
 @pytest.mark.parametrize("which", [(1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 0, 1), (0, 1, 1)])
-@pytest.mark.parametrize("T", [5, 50])
+@pytest.mark.parametrize("T", [5, 50, 90, 110, 190])
 def test_router_bwd_few_tokens_parts(T, which):
     check_router(T, 192, 24, *map(bool, which))
 
@@ -473,6 +473,7 @@ def test_router_bwd_few_tokens_parts(T, which):
 @pytest.mark.parametrize("scale", [1e-30, 3e-34, 1e30])
 def test_router_bwd_few_tokens_tiny_and_huge_gradients(scale):
     check_router(40, 128, 20, scale=scale)
+    check_router(180, 64, 12, scale=scale)
 
 
 def test_router_bwd_few_tokens_same_bits_and_unaligned():
