@@ -12,15 +12,11 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib
 import os
 from typing import Optional
 
 import torch
-
-try:
-    from . import _operands as _native  # csrc/operands.cpp
-except ImportError as err:  # not built, or for another torch: load_library says so
-    _native, _native_error = None, err
 
 LIB_NAME = "libmoe_b200.so"
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), LIB_NAME)
@@ -84,10 +80,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         raise RuntimeError(
             f"{LIB_NAME} is not built (expected at {path}); run "
             "`python -m routing_dispatch_expert_softmax_b200.build`")
-    if _native is None:
-        raise RuntimeError("_operands.so is not built for this Python and torch; run "
-                           "`python -m routing_dispatch_expert_softmax_b200.build`"
-                           ) from _native_error
+    if _native is None:  # perhaps built since the package was imported
+        try:
+            _load_native()
+        except ImportError as err:
+            raise RuntimeError("_operands.so is not built for this Python and torch; run "
+                               "`python -m routing_dispatch_expert_softmax_b200.build`") from err
     if _native.TORCH != str(torch.__version__).split("+")[0]:
         raise RuntimeError(f"_operands.so is built for torch {_native.TORCH}; run "
                            "`python -m routing_dispatch_expert_softmax_b200.build`")
@@ -507,16 +505,11 @@ def moe_forward_fp8_staged(x, w_g, bias, w13, w13_scale, w2, w2_scale, y, shape:
 
 
 # ------------------------------------------------------- training the gate
-class _NotBuilt:
-    def __init__(self, where):
-        load_library()  # raises
-
-
-class _Operands(_native.Operands if _native else _NotBuilt):
-    """The tensors of one call: ``ptr(t, dtype, shape, name, optional)`` checks
-    one (CUDA, dtype, shape, contiguity, the call's one device) and gives its
-    address; ``launch`` runs the call on that device and the stream asked for
-    (default: the device's current one)."""
+class _OperandCalls:
+    """The tensors of one call (with csrc/operands.cpp's Operands): ``ptr(t,
+    dtype, shape, name, optional)`` checks one (CUDA, dtype, shape, contiguity,
+    the call's one device) and gives its address; ``launch`` runs the call on
+    that device and the stream asked for (default: the device's current one)."""
 
     __slots__ = ()
 
@@ -559,6 +552,27 @@ class _Operands(_native.Operands if _native else _NotBuilt):
                 status = fn(*args, handle)
         if status != MOE_OK:
             raise MoEError(status, self.where)
+
+
+_native = None
+
+
+def _load_native():
+    global _native, _Operands
+    importlib.invalidate_caches()
+    _native = importlib.import_module("._operands", __package__)
+    _Operands = type("_Operands", (_OperandCalls, _native.Operands), {"__slots__": ()})
+
+
+def _Operands(where):  # until the extension is built
+    load_library()  # loads it, or raises
+    return _Operands(where)
+
+
+try:
+    _load_native()
+except ImportError:
+    pass
 
 
 @functools.lru_cache(maxsize=1024)
@@ -736,7 +750,7 @@ class GradList:
         self.device = torch.device("cuda", o.index)
         self._seen = seen
 
-    def operands(self, where: str) -> _Operands:
+    def operands(self, where: str) -> _OperandCalls:
         self._refresh()
         o = _Operands(where)
         o.index = self.index

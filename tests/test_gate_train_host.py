@@ -4,6 +4,7 @@ Python binding.  Nothing here reaches a kernel."""
 
 import ctypes
 import math
+import subprocess
 import sys
 
 import numpy as np
@@ -296,3 +297,28 @@ def test_addresses(lib):
         B._native.addresses(ts, ts)
     after = sys.getrefcount(ts[0])
     assert after == before
+
+
+def test_extension_found_after_import(lib):
+    # a process that imported the package before the extension was built finds it later
+    code = ("import importlib, torch\n"
+            "real = importlib.import_module\n"
+            "def hide(name, *a):\n"
+            "    if name.endswith('_operands'): raise ImportError(name)\n"
+            "    return real(name, *a)\n"
+            "importlib.import_module = hide\n"
+            "import routing_dispatch_expert_softmax_b200 as moe\n"
+            "from routing_dispatch_expert_softmax_b200 import binding as B\n"
+            "assert B._native is None\n"
+            "s = moe.MoEShape.of(1, 64, 1, 1, 64)\n"
+            "for _ in range(2):\n"
+            "    try: moe.moe_combine_bwd(None, None, None, None, s)\n"
+            "    except RuntimeError as e: assert '_operands.so is not built' in str(e)\n"
+            "    else: assert False\n"
+            "importlib.import_module = real\n"
+            "try: moe.moe_combine_bwd(None, None, None, None, s)\n"
+            "except TypeError as e: assert 'dy is required' in str(e)\n"
+            "else: assert False\n"
+            "assert B._native is not None\n")
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert p.returncode == 0, p.stderr
