@@ -704,8 +704,9 @@ __global__ void __launch_bounds__(256) k_router_sum(const float* __restrict__ pa
 //   dx: 16 tokens x 8 columns a tile, K = experts, both rounded to tf32 (2^-11 of each
 //       value, as fp16 keeps in the large path; no scaling, tf32 has fp32's range).
 // Rows lie ep = 4 (mod 32) words apart: the 8 x 4 lanes of a fragment hit 32 banks.
-// Every block reads all of dL from L2, which is most of the time (64 x 2048 x 128: 6.0
-// us, 3.5 with 16 tokens; 8 warps a block in place of 16 took 3 us more).
+// 64 x 2048 x 128: 6.0 us, 3.5 with 16 tokens.  What bounds it is one latency after the
+// other: the loads and the barrier behind them, new code's fetch, the MMAs, the stores
+// (issue slots 36% used, L2 7%); 8 warps a block in place of 16 took 3 us more.
 struct RouterSmallArgs {
   const __nv_bfloat16* x;
   const float* w;
