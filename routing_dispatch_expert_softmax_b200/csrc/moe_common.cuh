@@ -199,8 +199,8 @@ struct BwdLayout {
   // pair that meets (at most blocks + S of them)
   int chunk;
   size_t prob, count, z, n, term, zterm;
-  // router backward: bf16 planes of dlogits (router_planes), fp16 dlogits [T][cp]
-  // and w_g [d][cp] (cp = E rounded up to 64) with the factors that undo their rows'
+  // router backward: bf16 planes of dlogits (router_planes), dlogits [T][2][cp] and
+  // w_g [d][2][cp] in two fp16 parts (cp = E rounded up to 64) with the factors that undo their rows'
   // scaling, column sums of every plane_rows tokens, and (last) partial weight
   // gradients of the token ranges
   int cp, plane_rows;
@@ -225,14 +225,16 @@ inline RouterPlanes router_planes(int E, int T) {
 
 // Times in us that the router's backward plans with, as measured: a 64-token block
 // of a 128 x 256 tile of dW (the MMAs, or for one set the 32 KB of x); a 128 x 256
-// tile of dx (its 64 KB of output; from 256 experts on the MMAs, and above that W's
-// tiles too, which the shared memory then does not keep); an item's start and end.
+// tile of dx (its 64 KB of output up to 64 experts, the MMAs from there on, and above
+// 128 W's tiles too, which the shared memory then does not keep; alone a tile takes a
+// quarter more, but of seven factors this one gave the least times beside dW over
+// eleven shapes); an item's start and end.
 inline double router_dw_block_us(int sets) {
   return sets == 3 ? 1.1 : sets == 2 ? 0.85 : 0.68;
 }
 inline double router_dx_tile_us(int E) {
   const int kx = (E + 63) / 64;
-  return kx <= 4 ? std::max(1.5, 0.5 * kx) : 0.62 * kx;
+  return kx == 1 ? 1.6 : kx == 2 ? 2.1 : 1.15 * kx;
 }
 constexpr double kRouterItemUs = 2.0;
 
@@ -301,8 +303,8 @@ inline BwdLayout bwd_layout(const moe_shape& s, int S) {
   L.plane_rows = T <= 64 ? 64 : (int)std::max(32LL, (T + 591) / 592);
   const RouterPlanes pl = router_planes(s.E, s.T);
   L.dl_planes = take(2 * (size_t)T * pl.width * (pl.sets == 3 ? 3 : 4));
-  L.dl_half = take(2 * (size_t)T * L.cp);
-  L.w_half = take(2 * (size_t)d * L.cp);
+  L.dl_half = take(4 * (size_t)T * L.cp);
+  L.w_half = take(4 * (size_t)d * L.cp);
   L.dl_back = take(2 * (size_t)T);
   L.w_back = take(2 * (size_t)d);
   L.db_part = take(sizeof(float) * (size_t)((T + L.plane_rows - 1) / L.plane_rows) * E);

@@ -6,20 +6,22 @@
 //   dW: dL splits into three bf16 planes of 8 bits each, hi + mid + lo = v.  x is
 //       bf16, so the three products are exact and dW is as good as an fp32
 //       product's;
-//   dx: dx is rounded to bf16 (2^-8), so dL and W are rounded to fp16, which
-//       keeps 2^-11 of each value: a third of the MMAs that planes of both
-//       would take.  Each row is first scaled by a power of two that brings
-//       its largest value to [2^14, 2^15), so that no value overflows and only
-//       those below 2^-28 of the row's largest lose bits; the epilogue scales back.
+//   dx: dL and W split into two fp16 parts of 11 bits each, of which lo lo, 2^-22 of
+//       a product, is left out.  One part would be a third of the MMAs, but where terms
+//       cancel (a softmax's gradients sum to zero over a row, and W's columns may
+//       have much in common) its 2^-11 and not bf16's 2^-8 is the error that remains.
+//       Each row is first scaled by a power of two that brings its largest value to
+//       [2^14, 2^15), so that no value overflows and only those below 2^-17 of the row's
+//       largest lose bits (2^-39 of it at most); the epilogue scales back.
 // One persistent kernel then runs the tiles of both products.  The tokens are
 // the long axis of dW, so its tiles split over token ranges; a last kernel
 // adds the ranges' partial tiles in order.  Few tokens take one kernel of their own.
 //
-// 16384 x 7168 x 256: 210 us (240 GFLOP of 16-bit products: dW's three, dx's one),
-// of which the products take 182 with the tensor pipe 66% active, and 247 us back to
-// back, where the power limit sets the clock.  8192 x 2048 x 128: 34.5 us, the products
-// 22 (a third of it MMAs; the rest is each item's start and end, 2 us, and dx's way
-// out through TMEM), the operands' kernel 5 and the sum 4.
+// 16384 x 7168 x 256: 306 us (361 GFLOP of 16-bit products, dW's three and dx's three a
+// term: 259 at the rate that the power limit leaves a library product), of which dW
+// alone is 156 and dx alone 159, and 361 us back to back.  8192 x 2048 x 128: 38 us,
+// dW alone 23 and dx alone 18 (the operands' kernel and the sum are 5 and 4 of it, an
+// item's start and end 2).
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -66,9 +68,9 @@ __device__ __forceinline__ void half_scale(float top, float& scale, float& back)
 //   planes                its bf16 planes: plane p of row r at r * row + p * plane,
 //                         `width` columns (zeros from cols on); with zero_plane a
 //                         fourth of zeros
-//   half [rows][cp], back [rows]  its rows scaled and rounded to fp16, cp = cols
-//                         rounded up to 64 with zeros, and the factors that undo
-//                         the scaling
+//   half [rows][2][cp], back [rows]  its rows scaled, in two fp16 parts (rounded, and
+//                         the rounded rest), cp = cols rounded up to 64 with zeros,
+//                         and the factors that undo the scaling
 //   sums [block][cols]    column sums of each block's rows
 struct PlanesArgs {
   const float* a;
@@ -142,14 +144,19 @@ __device__ void planes_block(const PlanesArgs& p, int block, float* red) {
               make_uint4(0, 0, 0, 0);
       }
       if (p.half) {
-        uint32_t w[4];
+        uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const __half2 h = __floats2half2_rn(v[n][2 * i] * scale, v[n][2 * i + 1] * scale);
-          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+          const float a = v[n][2 * i] * scale, b = v[n][2 * i + 1] * scale;
+          const __half2 h = __floats2half2_rn(a, b);
+          const float2 f = __half22float2(h);
+          const __half2 rest = __floats2half2_rn(a - f.x, b - f.y);  // the differences are exact
+          hi[i] = *reinterpret_cast<const uint32_t*>(&h);
+          lo[i] = *reinterpret_cast<const uint32_t*>(&rest);
         }
-        *reinterpret_cast<uint4*>(p.half + (size_t)r * p.cp + c0) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+        __half* to = p.half + (size_t)r * 2 * p.cp + c0;
+        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(to + p.cp) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
   }
@@ -185,15 +192,15 @@ __global__ void __launch_bounds__(256) k_router_planes(const PlanesArgs dl, cons
 //   dW: rows = 128 experts, columns = 256 of d, K = the tokens of one range;
 //       A = dL planes and B = x, both with the non-K index contiguous
 //       (MN-major): tiles of 64 tokens x 64 columns, 128 bytes a row;
-//   dx: rows = 128 tokens, columns = 256 of d, K = experts; A = dL and B = W in
-//       fp16, both K-major.
+//   dx: rows = 128 tokens, columns = 256 of d, K = experts; A = dL and B = W in two
+//       fp16 parts each, all K-major: lo hi, hi lo and hi hi (the small ones first).
 // dW takes the experts as rows so that a row of 256 columns of x serves the
 // three planes, and a lane's accumulator row is one expert: the 32 lanes of a
 // warp then store 32 neighbouring experts of dW[i, :].
 // Shared memory: a ring of 16 KB A tiles and one of 32 KB B tiles (128-byte
-// swizzle).  For each 64 of K, dW takes `sets` A (RouterPlanes) and 1 B tiles, dx one of each; with
-// up to 256 experts a block keeps the W tiles of its 256 columns in the B ring
-// while it goes down the tokens, so that a dx item loads 64 KB at most.
+// swizzle).  For each 64 of K, dW takes `sets` A (RouterPlanes) and 1 B tiles, dx two of
+// each; with up to 128 experts a block keeps the W tiles of its 256 columns in the B
+// ring while it goes down the tokens, so that a dx item loads 64 KB at most.
 //
 // The tensor cores cut, not round, when they add to an fp32 accumulator, so a
 // sum is short by about 2^-25 of itself for every MMA in a row (measured: dW
@@ -389,17 +396,20 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
       }
       int nt = dx0 / args.mt, mt = dx0 - nt * args.mt;
       for (int w = dx0; w < dx1 && ok; ++w) {
-        const bool load_b = args.kx > rb || w == dx0 || mt == 0;
-        for (int kb = 0; kb < args.kx && ok; ++kb) {
-          uint8_t* dst = take_a();
+        const bool load_b = 2 * args.kx > rb || w == dx0 || mt == 0;
+        for (int i = 0; i < 2 * args.kx && ok; ++i) {  // W hi, dL lo; W lo, dL hi
+          const int hi = (i >> 1) * 64, lo = hi + args.kx * 64;
+          uint8_t* dst;
+          if (load_b) {
+            dst = take_b();
+            if (!(ok = dst != nullptr)) break;
+            tma_load_2d(dst, &tm_w, &b_full[b.slot], i & 1 ? lo : hi, nt * 256, policy);
+            b.next(rb);
+          }
+          dst = take_a();
           if (!(ok = dst != nullptr)) break;
-          tma_load_2d(dst, &tm_dl_k, &a_full[a.slot], kb * 64, mt * 128, policy);
+          tma_load_2d(dst, &tm_dl_k, &a_full[a.slot], i & 1 ? hi : lo, mt * 128, policy);
           a.next(kRA);
-          if (!load_b) continue;
-          dst = take_b();
-          if (!(ok = dst != nullptr)) break;
-          tma_load_2d(dst, &tm_w, &b_full[b.slot], kb * 64, nt * 256, policy);
-          b.next(rb);
         }
         if (++mt == args.mt) mt = 0, ++nt;
       }
@@ -468,7 +478,7 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
       }
       // W's tiles stay until the last item of a block of columns (or, with too
       // many experts for the ring, are new for each item).
-      const bool keep = args.kx <= rb;
+      const bool keep = 2 * args.kx <= rb;
       Ring b0;
       int mt = dx0 < dx1 ? dx0 % args.mt : 0;
       for (int w = dx0; w < dx1 && ok; ++w, ++it) {
@@ -481,16 +491,30 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
         const bool free_b = !keep || w + 1 == dx1 || mt == 0;
         if (new_b) b0 = b;
         b = b0;
+        auto products = [&](uint64_t da, uint64_t db, bool first) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 16 K columns of 2 bytes each
+            umma_bf16_ss(d, da + kk * (32 >> 4), db + kk * (32 >> 4), kIdescK,
+                         first && kk == 0 ? 0u : 1u);
+        };
         for (int kb = 0; kb < args.kx; ++kb) {
           if (new_b && !(ok = wait(&b_full[b.slot], b.phase))) break;
           if (!(ok = wait(&a_full[a.slot], a.phase))) break;
-          const uint64_t da = a_k + a.slot * kA, db = b_k + b.slot * kB;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 16 K columns of 2 bytes each
-            umma_bf16_ss(d, da + kk * (32 >> 4), db + kk * (32 >> 4), kIdescK, (kb | kk) ? 1u : 0u);
+          const int hi = b.slot;
+          const uint64_t w_hi = b_k + hi * kB;
+          products(a_k + a.slot * kA, w_hi, kb == 0);
           umma_commit(&a_empty[a.slot]);
           a.next(kRA);
+          b.next(rb);
+          if (new_b && !(ok = wait(&b_full[b.slot], b.phase))) break;
+          if (!(ok = wait(&a_full[a.slot], a.phase))) break;
+          const uint64_t dl_hi = a_k + a.slot * kA;
+          products(dl_hi, b_k + b.slot * kB, false);
           if (free_b) umma_commit(&b_empty[b.slot]);
+          products(dl_hi, w_hi, false);
+          umma_commit(&a_empty[a.slot]);
+          a.next(kRA);
+          if (free_b) umma_commit(&b_empty[hi]);
           b.next(rb);
         }
         if (ok) umma_commit(&tfull[ab]);
@@ -701,10 +725,10 @@ __global__ void __launch_bounds__(256) k_router_sum(const float* __restrict__ pa
 // x [T][16] in shared memory.
 //   dW: 16 columns x 8 experts a tile, K = tokens, x in bf16, dL in three bf16 planes
 //       with a sum each, added last;
-//   dx: 16 tokens x 8 columns a tile, K = experts, both rounded to tf32 (2^-11 of each
-//       value, as fp16 keeps in the large path; no scaling, tf32 has fp32's range).
+//   dx: 16 tokens x 8 columns a tile, K = experts, both in two tf32 parts (split2: 2^-21
+//       of each value is lost), hi lo and lo hi with a sum of their own, added last.
 // Rows lie ep = 4 (mod 32) words apart: the 8 x 4 lanes of a fragment hit 32 banks.
-// 64 x 2048 x 128: 6.0 us, 3.5 with 16 tokens.  What bounds it is one latency after the
+// 64 x 2048 x 128: 6.6 us, 3.7 with 16 tokens.  What bounds it is one latency after the
 // other: the loads and the barrier behind them, new code's fetch, the MMAs, the stores
 // (issue slots 36% used, L2 7%); 8 warps a block in place of 16 took 3 us more.
 struct RouterSmallArgs {
@@ -758,10 +782,17 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t to_tf32(float v) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
-  return r;
+// v = hi + lo in tf32 (11 bits each): hi has the upper bits of the mantissa as they stand,
+// so it cannot overflow, the rest is exact and is rounded.  A product of two such values
+// leaves lo lo out (2^-20 of it at most).  inf and NaN leave NaN in the rest.
+struct Split2 {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Split2 split2(float v) {
+  Split2 s;
+  s.hi = __float_as_uint(v) & 0xffffe000u;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(s.lo) : "f"(v - __uint_as_float(s.hi)));
+  return s;
 }
 __device__ __forceinline__ uint32_t pair_of(__nv_bfloat16 lo, __nv_bfloat16 hi) {
   const __nv_bfloat162 v = __halves2bfloat162(lo, hi);
@@ -839,20 +870,26 @@ __global__ void __launch_bounds__(32 * kSmallWarps, KS <= 4 ? 2 : 1)
     // a warp takes 16 tokens, and with fewer than 8 such tiles a part of the experts
     constexpr int tiles = KS, parts = kSmallWarps / tiles;
     const int mt = warp % tiles, part = warp / tiles;
-    float c[2][4] = {};
+    float c[2][4] = {}, cs[2][4] = {};
     if (part < parts) {
       const int n8 = E8 / 8;
       const float* pa = sdl + (16 * mt + g) * a.ep + t4;
       const float* pb = sw + g * a.ep + t4;
 #pragma unroll 4
       for (int k = part; k < n8; k += parts) {
-        uint32_t f[4];
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = to_tf32(pa[(i & 1) * 8 * a.ep + 8 * k + (i >> 1) * 4]);
+        for (int i = 0; i < 4; ++i) {
+          const Split2 v = split2(pa[(i & 1) * 8 * a.ep + 8 * k + (i >> 1) * 4]);
+          hi[i] = v.hi, lo[i] = v.lo;
+        }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const float* q = pb + 8 * n * a.ep + 8 * k;
-          mma_tf32(c[n], f, to_tf32(q[0]), to_tf32(q[4]));
+          const Split2 u = split2(q[0]), v = split2(q[4]);
+          mma_tf32(cs[n], lo, u.hi, v.hi);
+          mma_tf32(c[n], hi, u.hi, v.hi);
+          mma_tf32(cs[n], hi, u.lo, v.lo);
         }
       }
     }
@@ -860,7 +897,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps, KS <= 4 ? 2 : 1)
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        meet[warp * 256 + (g + (i >> 1) * 8) * 16 + 8 * n + 2 * t4 + (i & 1)] = c[n][i];
+        meet[warp * 256 + (g + (i >> 1) * 8) * 16 + 8 * n + 2 * t4 + (i & 1)] = c[n][i] + cs[n][i];
     __syncthreads();
     for (int q = threadIdx.x; q < 8 * a.T; q += 32 * kSmallWarps) {  // a pair of columns each
       const int t = q >> 3, i = 2 * (q & 7);
@@ -896,11 +933,11 @@ size_t router_small_smem(const moe_shape& s) {
          2 * T16 * kSmallXPitch;
 }
 // Where the blocks of 16 columns fit the GPU at once (two an SM up to 64 tokens): E = 8
-// to 256, d = 512 to 4096, 16 to 64 tokens took 2.7 to 10.3 us where the three kernels
-// took 7.6 to 13.2, d = 512 and 2048, 96 to 192 tokens 4.8 to 10.3 in place of 10.2 to
-// 13.8, less in each.  In a second wave each block loads dL again: up to 32 tokens still
-// won (d = 7168: 4.9 to 10.6 against 8.1 to 12.4), 64 did at no E but 8 (16.0 against
-// 14.2 with 256 experts).
+// to 256, d = 512 to 4096, 16 to 64 tokens took 2.7 to 11.9 us where the three kernels
+// took 7.6 to 18.8, d = 512 and 2048, 96 to 192 tokens 4.9 to 11.5 in place of 10.3 to
+// 14.0, less in each.  In a second wave each block loads dL again: up to 32 tokens still
+// won (d = 7168: 5.2 to 12.0 against 8.2 to 18.3), 64 did at no E but 8 (16.0 against
+// 14.2 with 256 experts, when dx took one product a term in both).
 bool router_small(const moe_shape& s, int sms) {
   if (s.T > kSmallT || router_small_smem(s) > kSmallSmem) return false;
   const int resident = s.T <= 64 && router_small_smem(s) <= kSmallSmem2 ? 2 * sms : sms;
@@ -1005,7 +1042,7 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
     RouterGemmArgs a{};
     a.T = T, a.d = d, a.E = E;
     a.sets = pl.sets, a.parts = pl.parts;
-    a.rb = cp <= 128 ? 3 : kRB;
+    a.rb = cp <= (dx ? 64 : 128) ? 3 : kRB;
     a.ne = apart ? (E + 127) / 128 : 1, a.nd = (d + 255) / 256;
     a.kblocks = kblocks, a.kper = kper;
     a.dw_items = dw ? a.ne * a.nd * ranges : 0;
@@ -1023,12 +1060,12 @@ cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const fl
     a.light_dx = heavy == 0 ? a.dx_items
                             : (int)std::min<double>(a.dx_items, light * (level + more) + 0.5);
     a.dw = direct ? dw : part, a.err = reinterpret_cast<int*>(ws);
-    const uint64_t row = (uint64_t)cp * 2;
+    const uint64_t row = (uint64_t)cp * 4;
     CUtensorMap mx{}, mn{}, mk{}, mw{}, mdx{};
     const uint64_t xd[3] = {64, (uint64_t)T, (uint64_t)d / 64}, xs[2] = {(uint64_t)d * 2, 128};
     const uint64_t nd[4] = {64, (uint64_t)T, (uint64_t)prow / 64, apart ? 3u : 1u};
     const uint64_t ns[3] = {(uint64_t)prow * 2, 128, (uint64_t)prow * 2 * T};
-    const uint64_t kd[2] = {(uint64_t)cp, (uint64_t)T}, wd[2] = {(uint64_t)cp, (uint64_t)d};
+    const uint64_t kd[2] = {2 * (uint64_t)cp, (uint64_t)T}, wd[2] = {2 * (uint64_t)cp, (uint64_t)d};
     const uint64_t od[2] = {(uint64_t)d, (uint64_t)T}, os[1] = {(uint64_t)d * 2};
     const uint32_t xb[3] = {64, 64, 4}, nb[4] = {64, 64, 2, 1}, kb[2] = {64, 128},
                    wb[2] = {64, 256}, ob[2] = {32, 32};
