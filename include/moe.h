@@ -540,8 +540,9 @@ MOE_API int moe_combine_bwd(const moe_bf16* dy, const moe_bf16* z, const int32_t
  *   not all.  Overwritten, not added to (T = 0 gives zeros).
  * dw_g is an fp32 product's (dlogits as three bf16 planes, which hold 24 bits, on
  * the tensor cores; sums in fp32).  For dx, dlogits and w_g are two parts of 11 bits,
- * and a term is off by 2^-19 of itself at most: with few tokens tf32 parts, else fp16
- * ones (rows scaled by powers of two; parts may also lose 2^-39 of their row's largest).
+ * and a term is off by 2^-19 of itself at most: with few tokens tf32 parts (a value may
+ * also lose 2^-137), else fp16 ones (rows scaled by powers of two; a value may also
+ * lose 2^-38 of its row's largest).
  * Where x, dlogits or w_g are not finite, so are the results
  * they reach (NaN in place of some infinities).
  *   ws moe_workspace_size_bwd(s, 1) bytes */

@@ -10,9 +10,9 @@
 //       a product, is left out.  One part would be a third of the MMAs, but where terms
 //       cancel (a softmax's gradients sum to zero over a row, and W's columns may
 //       have much in common) its 2^-11 and not bf16's 2^-8 is the error that remains.
-//       Each row is first scaled by a power of two that brings its largest value to
-//       [2^14, 2^15), so that no value overflows and only those below 2^-17 of the row's
-//       largest lose bits (2^-39 of it at most); the epilogue scales back.
+//       Each row is first scaled by an even power of two that brings its largest value
+//       to [2^13, 2^15), so that no value overflows and only those below 2^-16 of the
+//       row's largest lose bits (2^-38 of it at most); the epilogue scales back.
 // One persistent kernel then runs the tiles of both products.  The tokens are
 // the long axis of dW, so its tiles split over token ranges; a last kernel
 // adds the ranges' partial tiles in order.  Few tokens take one kernel of their own.
@@ -55,13 +55,13 @@ __device__ __forceinline__ Split3 split3(float a, float b) {
   return s;
 }
 
-// The power of two that brings |top| to [2^14, 2^15), and its inverse (1 for
-// 0, inf and NaN; at most 2^126, for rows below 2^-112).
+// The even power of two that brings |top| to [2^13, 2^15) (1 for 0, inf and NaN; at
+// most 2^126, for rows below 2^-112), and the square root of its inverse.
 __device__ __forceinline__ void half_scale(float top, float& scale, float& back) {
   const int e = (__float_as_int(top) >> 23) & 0xff;  // top >= 0; biased exponent
-  const int f = e == 255 || top == 0.f ? 0 : min(126, 127 + 14 - e);
-  scale = __int_as_float((f + 127) << 23);
-  back = __int_as_float((127 - f) << 23);
+  const int h = e == 255 || top == 0.f ? 0 : min(63, (127 + 14 - e) >> 1);
+  scale = __int_as_float((2 * h + 127) << 23);
+  back = __int_as_float((127 - h) << 23);
 }
 
 // One [rows, cols] fp32 matrix a; every output is optional:
@@ -70,7 +70,7 @@ __device__ __forceinline__ void half_scale(float top, float& scale, float& back)
 //                         fourth of zeros
 //   half [rows][2][cp], back [rows]  its rows scaled, in two fp16 parts (rounded, and
 //                         the rounded rest), cp = cols rounded up to 64 with zeros,
-//                         and the factors that undo the scaling
+//                         and the square roots of the factors that undo the scaling
 //   sums [block][cols]    column sums of each block's rows
 struct PlanesArgs {
   const float* a;
@@ -222,7 +222,7 @@ struct RouterGemmArgs {
   int mt;                // token tiles of dx
   int kx;                // 64-expert blocks of dx
   int light_dx;          // dx items of the blocks that have one dW item less
-  const __nv_bfloat16* dl_back;  // [T], [d]: factors that undo the fp16 scaling
+  const __nv_bfloat16* dl_back;  // [T], [d]: roots of the factors that undo the scaling
   const __nv_bfloat16* w_back;
   float* dw;             // [ranges][parts][d][E]
   int* err;
@@ -600,8 +600,12 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
       next_back = row_back(mt + 1 == args.mt ? 0 : mt + 1);
       if (!(ok = full())) break;
       const uint32_t t_addr = t_base + (uint32_t)((it & 1) * 256);
-      // The factors are powers of two, so they can follow the rounding to bf16,
-      // on pairs.  A step of 32 columns loads the next one's sums before it packs its own.
+      // The factors are powers of two, so they can follow the rounding to bf16, on pairs.
+      // The row's and the column's may lie far on either side of 1 while their product
+      // does not: their roots' product (2^-126 to 2^114) is multiplied with twice, so that
+      // what lies between is between the sum and the result, and passes no range before
+      // the result does.
+      // A step of 32 columns loads the next one's sums before it packs its own.
       uint32_t v[2][32];
       tmem_ld_32x32b_x32(t_addr, v[0]);
 #pragma unroll
@@ -623,7 +627,9 @@ __global__ void __launch_bounds__(kRouterThreads, 1) k_router_gemm(
           for (int j = 0; j < 4; ++j) {
             const uint32_t* u = v[n & 1] + 8 * i + 2 * j;
             __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(u[0]), __uint_as_float(u[1]));
-            y = __hmul2(__hmul2(y, back2), *reinterpret_cast<const __nv_bfloat162*>(&g[j]));
+            const __nv_bfloat162 m =
+                __hmul2(back2, *reinterpret_cast<const __nv_bfloat162*>(&g[j]));
+            y = __hmul2(__hmul2(y, m), m);
             o[j] = *reinterpret_cast<const uint32_t*>(&y);
           }
           // 64-byte swizzle: the 16-byte column of a row XOR bits 1 and 2 of the row
@@ -784,7 +790,8 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
 }
 // v = hi + lo in tf32 (11 bits each): hi has the upper bits of the mantissa as they stand,
 // so it cannot overflow, the rest is exact and is rounded.  A product of two such values
-// leaves lo lo out (2^-20 of it at most).  inf and NaN leave NaN in the rest.
+// leaves lo lo out (2^-20 of it at most); below 2^-114 lo nears tf32's lowest step, 2^-136.
+// inf and NaN leave NaN in the rest.
 struct Split2 {
   uint32_t hi, lo;
 };

@@ -48,8 +48,8 @@ def run(x, W, dl, dw=True, db=True, dx=True):
 def dx_bound(dl, W):
     """(dx in 64 bits, what the call may be off by).  Each operand is held in two parts of
     11 bits: what the second part loses (2^-21 of the value; for fp16 parts of a row that
-    was scaled to [2^13, 2^15) no less than 2^-25, 2^-38 of its largest) and the product
-    of the second parts (2^-20) come to 2^-19 of a term at most.  The tensor cores may cut
+    was scaled to [2^13, 2^15) no less than 2^-25, 2^-38 of its largest; for tf32 parts no
+    less than 2^-137, half of its lowest step) and the product of the second parts (2^-20) come to 2^-19 of a term at most.  The tensor cores may cut
     at each MMA, 2u of the sum and 2u of what is added: 12 MMAs for each 64 experts (or 8
     for the 64 of three products of 8), and 20 adds behind them."""
     E = W.shape[1]
@@ -57,6 +57,7 @@ def dx_bound(dl, W):
     ref, mag = l64 @ W64.t(), l64.abs() @ W64.abs().t()
     low = 2.0 ** -38 * (l64.abs().amax(1)[:, None] * W64.abs().sum(1)[None]
                         + l64.abs().sum(1)[:, None] * W64.abs().amax(1)[None])
+    low += 2.0 ** -137 * (W64.abs().sum(1)[None] + l64.abs().sum(1)[:, None])
     n = 24 * -(-E // 64) + 20
     return ref, BF16 * ref.abs() + (1 + BF16) * ((2.0 ** -19 + 4 * n * U32) * mag + low) + 1e-37
 
@@ -87,3 +88,44 @@ def test_dx_of_many_tokens_where_terms_cancel(T, d, E):
     ref, bound = dx_bound(dl, W)
     off = (run(x, W, dl, dw=E % 3 == 0)["dx"].double() - ref).abs()
     assert bool((off <= bound).all()), float((off / bound).max())
+
+
+@pytest.mark.parametrize("T,E", [(40, 24), (300, 24), (300, 60), (2000, 130), (300, 260)])
+@pytest.mark.parametrize("a,b", [(112, 0), (113, -15), (124, -20), (124, -124), (-100, 90), (-104, 115), (90, -99),
+                                 (-60, -46), (60, 60), (0, 120), (1, -90)])
+def test_dx_of_operands_far_from_one(T, E, a, b):
+    # the results lie in fp32's and bf16's range, whatever the operands' sizes
+    d = 128
+    g = torch.Generator(device=DEV).manual_seed(T + E)
+    x = torch.randn(T, d, generator=g, device=DEV).bfloat16()
+    W, dl = torch.randn(d, E, generator=g, device=DEV) / math.sqrt(d), torch.randn(T, E, generator=g, device=DEV)
+    one = run(x, W, dl, dw=False)["dx"]
+    dl, W = dl * 2.0 ** a, W * 2.0 ** b
+    got = run(x, W, dl, dw=False)["dx"]
+    ref, bound = dx_bound(dl, W)
+    off = (got.double() - ref).abs()
+    assert bool((off <= bound).all()), float((off / bound).max())
+    if a % 2 == b % 2 == 0 and a + b > -100 and min(a, b) >= -104:
+        # (below that the operands themselves round: fp32's lowest normal is 2^-126)
+        # rows are scaled by even powers of two: the same values go through the products
+        assert torch.equal(got.double(), one.double() * 2.0 ** (a + b))
+
+
+@pytest.mark.parametrize("T,E", [(300, 24), (700, 200)])
+def test_dx_of_rows_and_columns_of_every_size(T, E):
+    # one call whose rows and columns span fp32's range; a row of zeros and one far below the others
+    d = 192
+    g = torch.Generator(device=DEV).manual_seed(T)
+    x = torch.randn(T, d, generator=g, device=DEV).bfloat16()
+    up = torch.linspace(-110, 110, T, device=DEV).round()[:, None]
+    across = torch.linspace(100, -100, d, device=DEV).round()[:, None]
+    dl = torch.randn(T, E, generator=g, device=DEV) * torch.exp2(up)
+    W = torch.randn(d, E, generator=g, device=DEV) * torch.exp2(across)
+    dl[7], W[9] = 0, 0
+    dl[11] *= 2.0 ** -10
+    ref, bound = dx_bound(dl, W)
+    got = run(x, W, dl, dw=False)["dx"].double()
+    fits = ref.abs() < 2.0 ** 127
+    assert int(fits.sum()) > T * d // 2 and bool(torch.isfinite(got[fits]).all())
+    assert bool(((got - ref).abs() <= bound)[fits].all())
+    assert not got[7].any() and not got[:, 9].any()
