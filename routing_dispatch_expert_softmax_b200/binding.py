@@ -701,8 +701,7 @@ class GradList:
         if not self.grads:
             raise ValueError("GradList: no gradients")
         self.n = len(self.grads)
-        self._entries = (MoEGrad * self.n)()
-        self._seen = None
+        self._entries = self._seen = None
         lib = load_library()
         self._refresh()
         need = int(lib.moe_workspace_size_grads(self.n))
@@ -711,13 +710,14 @@ class GradList:
         self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
 
     def _refresh(self):
-        """Checks the tensors and fills the entries, unless no address has
-        changed since the last time."""
+        """Checks the tensors and makes the entries anew, unless no address has
+        changed since the last time.  What is refused leaves the list as it was."""
         seen = _native.addresses(self.grads, None if self.outs is self.grads else self.outs)
         if seen == self._seen:
             return
         o = _Operands("GradList")
-        for i, (g, out, e) in enumerate(zip(self.grads, self.outs, self._entries)):
+        entries = (MoEGrad * self.n)()
+        for i, (g, out, e) in enumerate(zip(self.grads, self.outs, entries)):
             if not isinstance(g, torch.Tensor) or g.dtype not in _GRAD_TYPES:
                 raise TypeError(f"GradList: gradient {i} must be an fp32 or bf16 tensor")
             if not isinstance(out, torch.Tensor) or out.dtype not in (g.dtype, torch.float32):
@@ -730,7 +730,7 @@ class GradList:
             e.n, e.dtype, e.out_dtype = g.numel(), _GRAD_TYPES[g.dtype], _GRAD_TYPES[out.dtype]
         # outs against everything else, by address
         spans = []
-        for i, e in enumerate(self._entries):
+        for i, e in enumerate(entries):
             if e.n:
                 spans.append((e.out, e.out + e.n * (2 if e.out_dtype else 4), i, True))
                 if e.data != e.out:
@@ -748,7 +748,7 @@ class GradList:
                 out_end, out_who = hi, i
         self.index = o.index
         self.device = torch.device("cuda", o.index)
-        self._seen = seen
+        self._entries, self._seen = entries, seen
 
     def operands(self, where: str) -> _OperandCalls:
         self._refresh()

@@ -1,0 +1,72 @@
+"""GradList's marshalled entries against the tensors they stand for, on the CPU: a stand-in
+for the operand checks accepts CPU tensors; nothing is launched."""
+
+import pytest
+import torch
+
+import routing_dispatch_expert_softmax_b200 as moe
+from routing_dispatch_expert_softmax_b200 import binding as B
+
+
+class Checks:
+    """What the native checks do, for CPU tensors; ``device`` is where they are said to lie."""
+
+    device = 0
+
+    def __init__(self, where):
+        self.where, self.index = where, None
+
+    def ptr(self, t, dtype, shape, name, optional=False):
+        if t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{self.where}: {name} must be contiguous")
+        self.index = Checks.device
+        return t.data_ptr()
+
+
+@pytest.fixture
+def cpu_list(monkeypatch):
+    B.load_library()
+    monkeypatch.setattr(B, "_Operands", Checks)
+    monkeypatch.setattr(Checks, "device", 0)
+    zeros = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, **kw: zeros(*a, **dict(kw, device="cpu")))
+    return moe.GradList
+
+
+def entries(lst):
+    return [(e.data, e.out, e.n, e.dtype, e.out_dtype) for e in lst._entries]
+
+
+def expected(tensors):
+    code = {torch.float32: 0, torch.bfloat16: 1}
+    return [(t.data_ptr(), t.data_ptr(), t.numel(), code[t.dtype], code[t.dtype]) for t in tensors]
+
+
+def test_entries_survive_a_refused_change(cpu_list):
+    a, b = torch.zeros(8, 8), torch.zeros(6, 4)
+    lst = cpu_list([a, b])
+    want = entries(lst)
+    assert want == expected([a, b])
+    old_a, old_b = a.data, b.data
+    a.data, b.data = torch.zeros(8, 8), torch.zeros(4, 6).t()  # b is refused, a alone would do
+    for _ in range(2):
+        with pytest.raises(ValueError, match="contiguous"):
+            lst.operands("call")
+    a.data, b.data = old_a, old_b
+    lst.operands("call")
+    assert entries(lst) == want
+    a.data = torch.zeros(8, 8)
+    lst.operands("call")
+    assert entries(lst) == expected([a, b])
+
+
+def test_entries_survive_a_refused_overlap(cpu_list):
+    a, b, buf = torch.zeros(50), torch.zeros(50), torch.zeros(100)
+    lst = cpu_list([a, b])
+    old_a, old_b = a.data, b.data
+    a.data, b.data = buf[:50], buf[40:90]
+    with pytest.raises(ValueError, match="overlaps"):
+        lst.operands("call")
+    a.data, b.data = old_a, old_b
+    lst.operands("call")
+    assert entries(lst) == expected([a, b])
