@@ -688,10 +688,10 @@ class GradList:
     its workspace so that a training loop marshals it once.  ``outs``: where
     the scaled gradients go, tensors of the same element counts, each of its
     gradient's dtype or fp32; default: in place.  No out may share memory with
-    another gradient or out.  The tensors' addresses are read again at every
-    call; their dtypes and element counts are not.  As with any workspace, calls
-    on one GradList must not run concurrently, and come after its making in
-    stream order."""
+    another gradient or out.  The tensors are looked at again at every call: what
+    they have become (their ``.data`` replaced) is what is scaled, or refused.
+    As with any workspace, calls on one GradList must not run concurrently, and
+    come after its making in stream order."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
@@ -710,9 +710,11 @@ class GradList:
         self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
 
     def _refresh(self):
-        """Checks the tensors and makes the entries anew, unless no address has
-        changed since the last time.  What is refused leaves the list as it was."""
-        seen = _native.addresses(self.grads, None if self.outs is self.grads else self.outs)
+        """Checks the tensors and makes the entries anew, unless they lie where they
+        lay the last time, as many of the same dtype.  What is refused leaves the
+        list as it was."""
+        outs = None if self.outs is self.grads else self.outs
+        seen = _native.addresses(self.grads, outs), _native.layouts(self.grads, outs)
         if seen == self._seen:
             return
         o = _Operands("GradList")

@@ -9,6 +9,8 @@
 //                    None for an optional t that is None.  Anything else goes to
 //                    ._refuse(t, dtype, shape, name), which a subclass has to raise in.
 //   addresses(a, b)  the data pointers of the lists' tensors (b may be None), as bytes
+//   layouts(a, b)  their element counts, dtypes, devices and whether they are contiguous,
+//                    as bytes to be compared with others
 //   TORCH            the version of torch that this was built against
 #include <Python.h>
 
@@ -17,6 +19,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
+#include <cstring>
 #include <exception>
 
 namespace {
@@ -128,16 +131,18 @@ PyGetSetDef operands_getset[] = {
     {nullptr, nullptr, nullptr, nullptr, nullptr}};
 PyTypeObject operands_type = {PyVarObject_HEAD_INIT(nullptr, 0)};
 
-PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t n) {
+// The bytes that fn makes of each of the lists' tensors, a list's after the other's.
+template <class T, class F>
+PyObject* each_tensor(PyObject* const* args, Py_ssize_t n, const char* usage, F&& fn) {
   if (n != 2 || !PyList_Check(args[0]) || (args[1] != Py_None && !PyList_Check(args[1]))) {
-    PyErr_SetString(PyExc_TypeError, "addresses(list, list or None)");
+    PyErr_SetString(PyExc_TypeError, usage);
     return nullptr;
   }
   const Py_ssize_t na = PyList_GET_SIZE(args[0]);
   const Py_ssize_t nb = args[1] == Py_None ? 0 : PyList_GET_SIZE(args[1]);
-  PyObject* out = PyBytes_FromStringAndSize(nullptr, (na + nb) * sizeof(void*));
+  PyObject* out = PyBytes_FromStringAndSize(nullptr, (na + nb) * sizeof(T));
   if (!out) return nullptr;
-  void** to = reinterpret_cast<void**>(PyBytes_AS_STRING(out));
+  char* to = PyBytes_AS_STRING(out);
   try {
     for (Py_ssize_t i = 0; i < na + nb; ++i) {
       PyObject* t = i < na ? PyList_GET_ITEM(args[0], i) : PyList_GET_ITEM(args[1], i - na);
@@ -146,7 +151,8 @@ PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t n) {
         PyErr_Format(PyExc_TypeError, "entry %zd is not a torch.Tensor", i < na ? i : i - na);
         return nullptr;
       }
-      to[i] = THPVariable_Unpack(t).data_ptr();
+      const T v = fn(THPVariable_Unpack(t));
+      std::memcpy(to + i * sizeof(T), &v, sizeof(T));
     }
   } catch (const std::exception& e) {
     Py_DECREF(out);
@@ -156,9 +162,30 @@ PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return out;
 }
 
+PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return each_tensor<void*>(args, n, "addresses(list, list or None)",
+                            [](const at::Tensor& t) { return t.data_ptr(); });
+}
+
+struct Layout {
+  int64_t elements;
+  int32_t dtype;
+  int16_t device, contiguous;
+};
+
+PyObject* layouts(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return each_tensor<Layout>(args, n, "layouts(list, list or None)", [](const at::Tensor& t) {
+    return Layout{t.numel(), static_cast<int32_t>(t.scalar_type()),
+                  static_cast<int16_t>(t.is_cuda() ? t.get_device() : -1),
+                  static_cast<int16_t>(t.is_contiguous())};
+  });
+}
+
 PyMethodDef module_methods[] = {
     {"addresses", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(addresses)), METH_FASTCALL,
      "The data pointers of the lists' tensors, as bytes."},
+    {"layouts", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(layouts)), METH_FASTCALL,
+     "The lists' tensors' element counts, dtypes, devices and contiguity, as bytes."},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_operands", "Operand checks of the binding.", -1,
                           module_methods, nullptr, nullptr, nullptr, nullptr};

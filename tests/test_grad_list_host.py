@@ -70,3 +70,55 @@ def test_entries_survive_a_refused_overlap(cpu_list):
     a.data, b.data = old_a, old_b
     lst.operands("call")
     assert entries(lst) == expected([a, b])
+
+
+def test_entries_follow_a_tensor_of_other_length_in_the_same_place(cpu_list):
+    buf = torch.zeros(64)
+    a, b = torch.zeros(0), torch.zeros(8)
+    a.data = buf
+    lst = cpu_list([a, b])
+    assert entries(lst)[0][2] == 64
+    a.data = buf[:10]  # a step's smaller gradient gets the old one's memory
+    lst.operands("call")
+    assert entries(lst) == expected([a, b]) and entries(lst)[0][2] == 10
+    a.data = buf[:32].view(4, 8)
+    lst.operands("call")
+    assert entries(lst)[0][2] == 32
+    a.data = buf[:32].view(4, 8).t()  # not contiguous any more: refused, in the same place too
+    with pytest.raises(ValueError, match="contiguous"):
+        lst.operands("call")
+
+
+def test_entries_follow_a_separate_out_of_other_length(cpu_list):
+    g, buf = torch.zeros(20), torch.zeros(64)
+    out = torch.zeros(0)
+    out.data = buf[:20]
+    lst = cpu_list([g], [out])
+    out.data = buf[:12]
+    with pytest.raises(ValueError, match="out 0 has 12 elements"):
+        lst.operands("call")
+    g.data = g.data[:12]
+    lst.operands("call")
+    assert entries(lst) == [(g.data_ptr(), buf.data_ptr(), 12, 0, 0)]
+
+
+def test_entries_follow_a_dtype_in_the_same_place(cpu_list):
+    buf = torch.zeros(64)
+    t = buf[:16]
+    lst = cpu_list([t])
+    lst.grads[0] = buf.view(torch.bfloat16)[:16]
+    lst.operands("call")
+    assert entries(lst) == expected([lst.grads[0]])
+
+
+def test_layouts():
+    B.load_library()
+    f = B._native.layouts
+    a, b = torch.zeros(4, 6), torch.zeros(4, 6)
+    assert f([a], None) == f([b], None) == f([a.view(24)], None)
+    others = [a[:3], a.bfloat16(), a.int(), a.t()]
+    assert len({f([t], None) for t in [a, *others]}) == 5
+    assert f([a, b], None) == f([a], [b]) == f([a], None) + f([b], None)
+    for args in (((), None), ([3], None), ([], [None]), ([], 3)):
+        with pytest.raises(TypeError):
+            f(*args)
