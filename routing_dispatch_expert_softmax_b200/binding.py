@@ -748,6 +748,9 @@ class GradList:
                 end, who = hi, i
             if is_out and hi > out_end:
                 out_end, out_who = hi, i
+        if self._seen is not None and o.index != self.index:
+            raise ValueError(f"GradList: the tensors are on cuda:{o.index}, the list was made on "
+                             f"cuda:{self.index}")
         self.index = o.index
         self.device = torch.device("cuda", o.index)
         self._entries, self._seen = entries, seen

@@ -122,3 +122,17 @@ def test_layouts():
     for args in (((), None), ([3], None), ([], [None]), ([], 3)):
         with pytest.raises(TypeError):
             f(*args)
+
+
+def test_tensors_on_another_device_are_refused(cpu_list):
+    # the list's workspace stays where it was made
+    a = torch.zeros(8)
+    lst = cpu_list([a])
+    Checks.device = 1
+    a.data = torch.zeros(8)
+    for _ in range(2):
+        with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
+            lst.operands("call")
+    Checks.device = 0
+    lst.operands("call")
+    assert entries(lst) == expected([a])
