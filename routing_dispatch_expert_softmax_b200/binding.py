@@ -1,8 +1,9 @@
 """Thin ctypes binding of ``libmoe_b200.so`` (the C ABI in ``include/moe.h``).
 
-Argument marshalling only (the checks of the calls that train the gate natively, in
-``_operands.so``): every step of the layer runs in the library's CUDA kernels.  Tensors are torch CUDA tensors (PyTorch supplies device memory and
-streams; the layer calls' y and moe_copy's operands may also be pinned host
+Argument marshalling only (the checks of the calls that train the gate
+natively, in ``_operands.so``, which the others do without): every step of the
+layer runs in the library's CUDA kernels.  Tensors are torch CUDA tensors
+(PyTorch supplies device memory and streams; the layer calls' y and moe_copy's operands may also be pinned host
 tensors); the functions keep the C names and raise :class:`MoEError` on a
 non-zero status.  There is no fallback: if the library is missing or the
 device is not an sm_100 GPU, calls raise.
@@ -80,15 +81,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         raise RuntimeError(
             f"{LIB_NAME} is not built (expected at {path}); run "
             "`python -m routing_dispatch_expert_softmax_b200.build`")
-    if _native is None:  # perhaps built since the package was imported
+    if _native is None:
         try:
             _load_native()
-        except ImportError as err:
-            raise RuntimeError("_operands.so is not built for this Python and torch; run "
-                               "`python -m routing_dispatch_expert_softmax_b200.build`") from err
-    if _native.TORCH != str(torch.__version__).split("+")[0]:
-        raise RuntimeError(f"_operands.so is built for torch {_native.TORCH}; run "
-                           "`python -m routing_dispatch_expert_softmax_b200.build`")
+        except ImportError:
+            pass  # only the calls that train the gate need it, and say so
     lib = ctypes.CDLL(path)
     lib.moe_error_string.restype = ctypes.c_char_p
     lib.moe_error_string.argtypes = [ctypes.c_int]
@@ -558,21 +555,24 @@ _native = None
 
 
 def _load_native():
+    """Imports the extension, which reads tensors as the torch that it was built
+    against lays them out: another one's is refused before it sees any."""
     global _native, _Operands
     importlib.invalidate_caches()
-    _native = importlib.import_module("._operands", __package__)
-    _Operands = type("_Operands", (_OperandCalls, _native.Operands), {"__slots__": ()})
+    native = importlib.import_module("._operands", __package__)
+    if native.TORCH != str(torch.__version__).split("+")[0]:
+        raise ImportError(f"built for torch {native.TORCH}, not {torch.__version__}")
+    _Operands = type("_Operands", (_OperandCalls, native.Operands), {"__slots__": ()})
+    _native = native
 
 
-def _Operands(where):  # until the extension is built
-    load_library()  # loads it, or raises
+def _Operands(where):  # until the extension is loaded
+    try:
+        _load_native()
+    except ImportError as err:
+        raise RuntimeError(f"_operands.so is not built for this Python and torch ({err}); run "
+                           "`python -m routing_dispatch_expert_softmax_b200.build`") from err
     return _Operands(where)
-
-
-try:
-    _load_native()
-except ImportError:
-    pass
 
 
 @functools.lru_cache(maxsize=1024)
@@ -703,6 +703,7 @@ class GradList:
         self.n = len(self.grads)
         self._entries = self._seen = None
         lib = load_library()
+        _Operands("GradList")  # raises without the extension
         self._refresh()
         need = int(lib.moe_workspace_size_grads(self.n))
         if need == 0:

@@ -1,0 +1,49 @@
+"""What of the package needs the Python extension of the operand checks: each in a process
+of its own."""
+
+import subprocess
+import sys
+
+HIDE = """
+import importlib, sys, types, torch
+real = importlib.import_module
+def fake(name, *a):
+    if name.endswith('_operands'):
+        if module is None: raise ImportError('no such file')
+        return module
+    return real(name, *a)
+importlib.import_module = fake
+module = None
+import routing_dispatch_expert_softmax_b200 as moe
+from routing_dispatch_expert_softmax_b200 import binding as B
+def refused(*words):
+    s = moe.MoEShape.of(1, 64, 1, 1, 64)
+    try: moe.moe_combine_bwd(None, None, None, None, s)
+    except RuntimeError as e:
+        for w in ('_operands.so is not built',) + words: assert w in str(e), e
+    else: assert False
+"""
+
+
+def run(code):
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert p.returncode == 0, p.stderr
+
+
+def test_importing_the_package_loads_no_native_code():
+    run("import sys\n"
+        "import routing_dispatch_expert_softmax_b200 as moe\n"
+        "assert not any(m.endswith('_operands') for m in sys.modules)\n"
+        "maps = open('/proc/self/maps').read()\n"
+        "assert '_operands.so' not in maps and 'libmoe_b200.so' not in maps\n")
+
+
+def test_the_library_without_the_extension():
+    run(HIDE + "lib = moe.load_library()\n"
+               "assert lib.moe_version() >= 105 and B.moe_error_string(0)\n"
+               "s = moe.MoEShape.of(4, 64, 8, 2, 64)\n"
+               "assert moe.moe_workspace_size(s) > 0 and moe.moe_workspace_size_bwd(s) > 0\n"
+               "refused()\n"
+               "try: moe.GradList([torch.zeros(3)])\n"
+               "except RuntimeError as e: assert '_operands.so is not built' in str(e), e\n"
+               "else: assert False\n")
