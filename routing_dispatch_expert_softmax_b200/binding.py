@@ -560,7 +560,7 @@ def _load_native():
     global _native, _Operands
     importlib.invalidate_caches()
     native = importlib.import_module("._operands", __package__)
-    if native.TORCH != str(torch.__version__).split("+")[0]:
+    if native.TORCH != str(torch.__version__):
         raise ImportError(f"built for torch {native.TORCH}, not {torch.__version__}")
     _Operands = type("_Operands", (_OperandCalls, native.Operands), {"__slots__": ()})
     _native = native

@@ -49,10 +49,11 @@ def _run(cmd):
 def build_operands(force: bool = False) -> str:
     """Compile the Python extension of the binding's checks against torch's headers."""
     import torch
-    # rebuilt for another torch: its tensors' layout belongs to one version
+    # rebuilt for another torch or Python: the objects' layouts belong to one version
     stamp = os.path.join(BUILD_DIR, "operands.torch")
+    versions = f"{torch.__version__} {sys.version_info[0]}.{sys.version_info[1]}"
     built_for = open(stamp).read() if os.path.exists(stamp) else ""
-    if (not force and os.path.exists(OPERANDS_OUT) and built_for == str(torch.__version__)
+    if (not force and os.path.exists(OPERANDS_OUT) and built_for == versions
             and os.path.getmtime(OPERANDS_OUT) > os.path.getmtime(OPERANDS_SRC)):
         return OPERANDS_OUT
     root = os.path.dirname(torch.__file__)
@@ -62,11 +63,12 @@ def build_operands(force: bool = False) -> str:
     tmp = OPERANDS_OUT + ".tmp"
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+          f'-DMOE_BUILT_FOR_TORCH="{torch.__version__}"',
           *(a for i in inc for a in ("-isystem", i)), OPERANDS_SRC, "-o", tmp,
           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
     os.replace(tmp, OPERANDS_OUT)
     with open(stamp, "w") as f:
-        f.write(str(torch.__version__))
+        f.write(versions)
     return OPERANDS_OUT
 
 

@@ -11,14 +11,16 @@
 //   addresses(a, b)  the data pointers of the lists' tensors (b may be None), as bytes
 //   layouts(a, b)  their element counts, dtypes, devices and whether they are contiguous,
 //                    as bytes to be compared with others
-//   TORCH            the version of torch that this was built against
+//   TORCH            the whole version of torch that this was built against (the header
+//                    has its first three numbers only)
+// Another Python than it was built for gets an ImportError.
 #include <Python.h>
 
 #include <structmember.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/version.h>
 
+#include <cstdio>
 #include <cstring>
 #include <exception>
 
@@ -193,6 +195,13 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_operands", "Operand checks of
 }  // namespace
 
 PyMODINIT_FUNC PyInit__operands() {
+  // objects' layouts belong to a minor version: look before any is made
+  int major = 0, minor = 0;
+  if (std::sscanf(Py_GetVersion(), "%d.%d", &major, &minor) != 2 || major != PY_MAJOR_VERSION ||
+      minor != PY_MINOR_VERSION) {
+    PyErr_Format(PyExc_ImportError, "built for Python %d.%d", PY_MAJOR_VERSION, PY_MINOR_VERSION);
+    return nullptr;
+  }
   operands_type.tp_name = "_operands.Operands";
   operands_type.tp_basicsize = sizeof(Operands);
   operands_type.tp_flags = Py_TPFLAGS_DEFAULT | Py_TPFLAGS_BASETYPE;
@@ -207,7 +216,7 @@ PyMODINIT_FUNC PyInit__operands() {
   if (!m) return nullptr;
   Py_INCREF(&operands_type);
   if (PyModule_AddObject(m, "Operands", reinterpret_cast<PyObject*>(&operands_type)) < 0 ||
-      PyModule_AddStringConstant(m, "TORCH", TORCH_VERSION) < 0) {
+      PyModule_AddStringConstant(m, "TORCH", MOE_BUILT_FOR_TORCH) < 0) {
     Py_DECREF(m);
     return nullptr;
   }

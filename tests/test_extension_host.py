@@ -1,8 +1,12 @@
-"""What of the package needs the Python extension of the operand checks: each in a process
-of its own."""
+"""What of the package needs the Python extension of the operand checks, and which build of
+it: each in a process of its own."""
 
 import subprocess
 import sys
+
+import torch
+
+from routing_dispatch_expert_softmax_b200 import binding as B
 
 HIDE = """
 import importlib, sys, types, torch
@@ -47,3 +51,30 @@ def test_the_library_without_the_extension():
                "try: moe.GradList([torch.zeros(3)])\n"
                "except RuntimeError as e: assert '_operands.so is not built' in str(e), e\n"
                "else: assert False\n")
+
+
+def test_an_extension_for_another_torch_is_refused_before_any_tensor():
+    run(HIDE + "class Never:\n"
+               "    def __init__(self, *a): raise SystemExit('made')\n"
+               "module = types.SimpleNamespace(TORCH='2.11.0.dev20260101+cpu', Operands=Never)\n"
+               "assert moe.load_library().moe_version() >= 105\n"
+               "refused('2.11.0.dev20260101+cpu', str(torch.__version__))\n"
+               "assert B._native is None\n")
+
+
+def test_a_prerelease_torch_has_an_extension_too():
+    for version in ("2.12.0a0+git1234567", "2.12.0.dev20260101", "2.11.0+vendor"):
+        run(HIDE + f"torch.__version__ = {version!r}\n"
+                   "class Operands:\n"
+                   "    __slots__ = ('where',)\n"
+                   "    def __init__(self, where): self.where = where\n"
+                   "    def ptr(self, t, *a): raise KeyError('seen')\n"
+                   f"module = types.SimpleNamespace(TORCH={version!r}, Operands=Operands)\n"
+                   "try: moe.moe_combine_bwd(None, None, None, None, moe.MoEShape.of(1, 64, 1, 1, 64))\n"
+                   "except KeyError: pass\n"
+                   "else: assert False\n")
+
+
+def test_the_built_extension_names_the_whole_version():
+    B.load_library()
+    assert B._native.TORCH == str(torch.__version__)
