@@ -1359,7 +1359,13 @@ __global__ void __launch_bounds__(192, 1) k_expert_gemm_swap(
 }
 
 // ============================================================== host side
-PFN_encodeTiled tensor_map_encoder() {
+typedef CUresult (*PFN_encodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
+                                    void*, const cuuint64_t*, const cuuint64_t*,
+                                    const cuuint32_t*, const cuuint32_t*,
+                                    CUtensorMapInterleave, CUtensorMapSwizzle,
+                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static PFN_encodeTiled get_encode() {
   static PFN_encodeTiled fn = nullptr;
   if (!fn) {
     void* p = nullptr;
@@ -1376,7 +1382,7 @@ PFN_encodeTiled tensor_map_encoder() {
 // (128 bytes, the swizzle span) x box_rows rows, 128-byte swizzle.
 static bool make_tmap(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t cols,
                       uint32_t box_rows) {
-  PFN_encodeTiled enc = tensor_map_encoder();
+  PFN_encodeTiled enc = get_encode();
   if (!enc) return false;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * 2};
@@ -1393,7 +1399,7 @@ static bool make_tmap(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t
 // matrix; box = 128 columns (128 bytes, the swizzle span) x box_rows rows.
 static bool make_tmap_u8(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t cols,
                          uint32_t box_rows) {
-  PFN_encodeTiled enc = tensor_map_encoder();
+  PFN_encodeTiled enc = get_encode();
   if (!enc) return false;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols};

@@ -5,6 +5,7 @@
 #include <climits>
 
 #include "moe_common.cuh"
+#include "moe_gate_train.cuh"
 
 namespace moe {
 
@@ -112,15 +113,6 @@ cudaError_t launch_combine_bwd(const __nv_bfloat16* dy, const __nv_bfloat16* z, 
 cudaError_t launch_router_bwd(const __nv_bfloat16* x, const float* w_g, const float* dl,
                               const moe_shape& s, float* dw, float* db, __nv_bfloat16* dx,
                               const BwdLayout& L, char* ws, int sms, cudaStream_t st);
-
-// cuTensorMapEncodeTiled, looked up once (moe_gemm_sm100.cu); nullptr if the
-// driver has none.
-typedef CUresult (*PFN_encodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
-                                    void*, const cuuint64_t*, const cuuint64_t*,
-                                    const cuuint32_t*, const cuuint32_t*,
-                                    CUtensorMapInterleave, CUtensorMapSwizzle,
-                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-PFN_encodeTiled tensor_map_encoder();
 
 // Global gradient norm and clipping (moe_grads.cu); the workspace holds the
 // header, a sum for moe_clip_grads, and the blocks' partial sums.

@@ -951,6 +951,20 @@ bool router_small(const moe_shape& s, int sms) {
   return s.d / 16 <= (s.T <= 32 ? 2 * resident : resident);
 }
 
+// cuTensorMapEncodeTiled, looked up once; nullptr if the driver has none.
+decltype(&cuTensorMapEncodeTiled) tensor_map_encoder() {
+  static const auto fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool found =
+        cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess;
+    return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(found ? p : nullptr);
+  }();
+  return fn;
+}
+
 // 16-bit tensor map of up to 4 dimensions, innermost first; strides in bytes of
 // dimensions 1 and up.
 bool make_map(CUtensorMap* tm, const void* base, int rank, const uint64_t* dims,
