@@ -11,14 +11,13 @@ import pytest
 import torch
 
 import routing_dispatch_expert_softmax_b200 as moe
-from routing_dispatch_expert_softmax_b200.binding import MoEShape
 
 from parity_utils import U32
+from router_utils import dw_bound, dx_bound, run
 
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
-BF16 = 2.0 ** -8
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -28,38 +27,6 @@ def _cuda():
     moe.load_library()
     yield
     torch.cuda.synchronize()
-
-
-def run(x, W, dl, dw=True, db=True, dx=True):
-    """The call's outputs, poisoned before; its scratch holds NaN patterns."""
-    T, d, E = x.shape[0], W.shape[0], W.shape[1]
-    s = MoEShape.of(T, d, E, 1, 64)
-    ws = moe.workspace_bwd(s)
-    ws[256:] = 0xff
-    out = dict(dw_g=torch.full((d, E), math.nan, device=DEV) if dw else None,
-               dbias=torch.full((E,), math.nan, device=DEV) if db else None,
-               dx=torch.full((T, d), math.nan, dtype=torch.bfloat16, device=DEV) if dx else None)
-    moe.moe_router_bwd(x if dw else None, W if dx else None, dl, s, ws, **out)
-    st = moe.moe_check(ws)
-    assert st == moe.MOE_OK, moe.moe_error_string(st)
-    return out
-
-
-def dx_bound(dl, W):
-    """(dx in 64 bits, what the call may be off by).  Each operand is held in two parts of
-    11 bits: what the second part loses (2^-21 of the value; for fp16 parts of a row that
-    was scaled to [2^13, 2^15) no less than 2^-25, 2^-38 of its largest; for tf32 parts no
-    less than 2^-137, half of its lowest step) and the product of the second parts (2^-20) come to 2^-19 of a term at most.  The tensor cores may cut
-    at each MMA, 2u of the sum and 2u of what is added: 12 MMAs for each 64 experts (or 8
-    for the 64 of three products of 8), and 20 adds behind them."""
-    E = W.shape[1]
-    l64, W64 = dl.double(), W.double()
-    ref, mag = l64 @ W64.t(), l64.abs() @ W64.abs().t()
-    low = 2.0 ** -38 * (l64.abs().amax(1)[:, None] * W64.abs().sum(1)[None]
-                        + l64.abs().sum(1)[:, None] * W64.abs().amax(1)[None])
-    low += 2.0 ** -137 * (W64.abs().sum(1)[None] + l64.abs().sum(1)[:, None])
-    n = 24 * -(-E // 64) + 20
-    return ref, BF16 * ref.abs() + (1 + BF16) * ((2.0 ** -19 + 4 * n * U32) * mag + low) + 1e-37
 
 
 def cancelling(T, d, E, seed=0):
@@ -129,3 +96,37 @@ def test_dx_of_rows_and_columns_of_every_size(T, E):
     assert int(fits.sum()) > T * d // 2 and bool(torch.isfinite(got[fits]).all())
     assert bool(((got - ref).abs() <= bound)[fits].all())
     assert not got[7].any() and not got[:, 9].any()
+
+
+# few tokens; planes side by side three and two to a row; a plane each; partial sums and none
+SHAPES = [(5, 64, 8), (150, 128, 24), (192, 64, 130), (300, 320, 24), (300, 192, 60), (200, 128, 60), (257, 320, 130),
+          (515, 128, 1000), (1000, 512, 128), (4097, 448, 60), (20000, 64, 8), (5000, 2048, 256)]
+
+
+@pytest.mark.parametrize("T,d,E", SHAPES)
+def test_dw_of_one_token_a_column_is_its_gradient(T, d, E):
+    # with a single 1 in each column of x the sum is one fp32 number: all its 24 bits arrive,
+    # in whichever token range and place of a tile the token lies
+    g = torch.Generator(device=DEV).manual_seed(T + E)
+    dl = torch.randn(T, E, generator=g, device=DEV) * torch.exp2(torch.randint(-30, 30, (T, E), generator=g, device=DEV))
+    W = torch.zeros(d, E, device=DEV)
+    for seed in range(3):
+        t = torch.randint(0, T, (d,), generator=g, device=DEV)
+        t[0], t[-1] = 0, T - 1
+        x = torch.zeros(T, d, dtype=torch.bfloat16, device=DEV)
+        x[t, torch.arange(d, device=DEV)] = 1.0
+        assert torch.equal(run(x, W, dl, dx=seed == 1)["dw_g"], dl[t])
+
+
+@pytest.mark.parametrize("T,d,E", [(192, 64, 8), (300, 192, 24), (3000, 16384, 256), (3000, 64, 130), (4097, 448, 60),
+                                   (20000, 64, 8), (20000, 4096, 200)])
+def test_dw_of_long_sums_of_one_sign(T, d, E):
+    # the tensor cores cut: left in their accumulator over 600 MMAs such a sum is 2.4e-5 short
+    g = torch.Generator(device=DEV).manual_seed(T + E)
+    x = (1 + torch.rand(T, d, generator=g, device=DEV)).bfloat16()
+    dl = 0.5 + torch.rand(T, E, generator=g, device=DEV)
+    got = run(x, torch.zeros(d, E, device=DEV), dl, dx=False)["dw_g"]
+    ref, bound = dw_bound(x, dl)
+    off = (got.double() - ref).abs()
+    assert bool((off <= bound).all()), float((off / ref).max())
+    assert float((bound / ref).max()) < 1.9e-5
