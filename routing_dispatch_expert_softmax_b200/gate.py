@@ -34,20 +34,33 @@ class GateTrainer:
     {balance + z, balance, z}, the selections of each expert in ``counts``
     (S, E), the counted tokens in ``tokens`` (S + 2,) and the mean
     probabilities in ``prob_mean`` (S, E); ``backward(dy)`` follows it, any
-    number of times, until the next forward."""
+    number of times, until the next forward.
+
+    A trainer's calls follow one another: on one stream, or on several that the
+    caller makes wait for each other.  Its workspaces grow to the largest batch
+    and serve all."""
 
     def __init__(self, layer: MoELayer, balance_coef: float = 1e-2, z_coef: float = 0.0):
         self.layer = layer
         self.balance_coef, self.z_coef = float(balance_coef), float(z_coef)
         self.loss = self.counts = self.tokens = self.prob_mean = None
         self._kept: Optional[dict] = None
-        self._ws: dict = {}
+        self._ws: dict = {"forward": None, "backward": None}
 
-    def _workspace(self, shape: B.MoEShape, S: int) -> torch.Tensor:
-        key = (shape.T, S)
-        if key not in self._ws:
-            self._ws[key] = B.workspace_bwd(shape, S, self.layer.w13.device)
-        return self._ws[key]
+    def _workspace(self, kind: str, need: int) -> torch.Tensor:
+        if need == 0:
+            raise B.MoEError(B.MOE_ERR_INVALID_ARG, "GateTrainer")
+        old = self._ws[kind]
+        if old is not None and old.numel() >= need:
+            return old
+        ws = torch.empty(need, dtype=torch.uint8, device=self.layer.w13.device)
+        if old is None:
+            ws[:64].zero_()  # the header; nothing else is read before it is written
+        else:
+            ws[:64].copy_(old[:64])  # with the error word
+            old.record_stream(torch.cuda.current_stream(old.device))
+        self._ws[kind] = ws
+        return ws
 
     def forward(self, x: torch.Tensor, token_mask: Optional[torch.Tensor] = None,
                 seq_offsets: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -58,8 +71,11 @@ class GateTrainer:
         if layer.physical_experts != layer.E:
             raise NotImplementedError("the gate trains without a replica plan")
         T, dev = int(x.shape[0]), layer.w13.device
-        shape, ws = layer.shape(T), layer.workspace(T)
         S = 1 if seq_offsets is None else len(seq_offsets) - 1
+        shape = layer.shape(T)
+        ws = self._workspace("forward", B.moe_workspace_size(shape))
+        bwd = B._bwd_bytes(T, layer.d, layer.E, layer.k, layer.f, layer.R, S)
+        ws_bwd = self._workspace("backward", bwd)
         new = lambda *size, dtype=torch.float32: torch.empty(*size, dtype=dtype, device=dev)  # noqa: E731
         E, k, d = layer.E, layer.k, layer.d
         logits, w = new(T, E), new(T, k)
@@ -79,12 +95,12 @@ class GateTrainer:
         B.moe_combine(z, row_of, w, y, shape)
         loss, counts, mean = new(3), new(S, E, dtype=torch.int32), new(S, E)
         tokens = new(S + 2, dtype=torch.int32)
-        B.moe_balance_loss(logits, idx, loss, counts, tokens, shape, self._workspace(shape, S),
+        B.moe_balance_loss(logits, idx, loss, counts, tokens, shape, ws_bwd,
                            balance_coef=self.balance_coef, z_coef=self.z_coef,
                            token_mask=token_mask, seq_offsets=seq_offsets, prob_mean=mean)
         self.loss, self.counts, self.tokens, self.prob_mean = loss, counts, tokens, mean
         self._kept = dict(x=x, logits=logits, idx=idx, w=w, row_of=row_of, z=z, shape=shape,
-                          mask=token_mask, seqs=seq_offsets, S=S, ws=ws)
+                          mask=token_mask, seqs=seq_offsets, ws=ws, ws_bwd=ws_bwd)
         return y
 
     __call__ = forward
@@ -101,7 +117,7 @@ class GateTrainer:
         q, layer = self._kept, self.layer
         shape, dev = q["shape"], layer.w13.device
         T, E, k, d = shape.T, layer.E, layer.k, layer.d
-        ws = self._workspace(shape, q["S"])
+        ws = q["ws_bwd"]
         dw = torch.empty(T, k, device=dev)
         dzt = torch.empty(T * k, d, dtype=torch.bfloat16, device=dev) if dz else None
         dlogits = torch.empty(T, E, device=dev)
@@ -125,5 +141,5 @@ class GateTrainer:
         if self._kept is None:
             return B.MOE_OK
         first = B.moe_check(self._kept["ws"], stream)
-        second = B.moe_check(self._workspace(self._kept["shape"], self._kept["S"]), stream)
+        second = B.moe_check(self._kept["ws_bwd"], stream)
         return first if first != B.MOE_OK else second
