@@ -38,7 +38,9 @@ class GateTrainer:
 
     A trainer's calls follow one another: on one stream, or on several that the
     caller makes wait for each other.  Its workspaces grow to the largest batch
-    and serve all."""
+    and serve all.  A captured step has workspaces of its own (forward and
+    backward are captured together), so that graphs can be replayed beside one
+    another and beside the trainer's further calls."""
 
     def __init__(self, layer: MoELayer, balance_coef: float = 1e-2, z_coef: float = 0.0):
         self.layer = layer
@@ -50,7 +52,8 @@ class GateTrainer:
     def _workspace(self, kind: str, need: int) -> torch.Tensor:
         if need == 0:
             raise B.MoEError(B.MOE_ERR_INVALID_ARG, "GateTrainer")
-        old = self._ws[kind]
+        captured = torch.cuda.is_current_stream_capturing()
+        old = None if captured else self._ws[kind]
         if old is not None and old.numel() >= need:
             return old
         ws = torch.empty(need, dtype=torch.uint8, device=self.layer.w13.device)
@@ -59,7 +62,8 @@ class GateTrainer:
         else:
             ws[:64].copy_(old[:64])  # with the error word
             old.record_stream(torch.cuda.current_stream(old.device))
-        self._ws[kind] = ws
+        if not captured:
+            self._ws[kind] = ws
         return ws
 
     def forward(self, x: torch.Tensor, token_mask: Optional[torch.Tensor] = None,

@@ -73,3 +73,50 @@ def test_error_word_outlives_a_larger_workspace(made):
     tr(t["x"])
     assert tr.check() == moe.MOE_ERR_DEVICE_CHECK
     assert tr.check() == moe.MOE_OK
+
+
+def capture(tr, x, dy, seqs):
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = tr(x, seq_offsets=seqs)
+        g = tr.backward(dy, dx=True, max_norm=1.0)
+    return graph, [t for t in (y, tr.loss, tr.counts, tr.tokens, tr.prob_mean, g.dw_g, g.dbias, g.dx, g.norm)
+                   if t is not None]
+
+
+def test_first_call_under_capture(made):
+    # the capture's own workspaces are set up by its replays, and eager calls have others
+    cfg, t, layer = made
+    x, dy = t["x"][:200].clone(), torch.randn(200, cfg.d, device=DEV).bfloat16()
+    seqs = offsets(200, 5)  # as long as the graph, like x and dy
+    want = step(moe.GateTrainer(layer), x, dy, seqs)
+    tr = moe.GateTrainer(layer)
+    graph, out = capture(tr, x, dy, seqs)
+    assert same(step(tr, x, dy, seqs), want)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(out, want)
+    assert same(step(tr, x, dy, seqs), want)
+    del graph, out
+    torch.cuda.empty_cache()
+    assert same(step(tr, x, dy, seqs), want) and tr.check() == moe.MOE_OK
+
+
+def test_two_captures_of_one_trainer_beside_each_other(made):
+    cfg, t, layer = made
+    xs = [t["x"].clone(), torch.randn(300, cfg.d, device=DEV).bfloat16()]
+    dy, seqs = torch.randn(300, cfg.d, device=DEV).bfloat16(), offsets(300, 6)
+    tr = moe.GateTrainer(layer, z_coef=1e-3)
+    want = [step(tr, x, dy, seqs) for x in xs]
+    made_graphs = [capture(tr, x, dy, seqs) for x in xs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (graph, _) in zip(streams, made_graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, out), w in zip(made_graphs, want):
+        assert same(out, w)
+    assert same(step(tr, xs[1], dy, seqs), want[1])
