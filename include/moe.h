@@ -466,6 +466,10 @@ MOE_API int moe_copy(void* dst, const void* src, int64_t bytes, void* stream);
  * time, as moe_workspace_size's. */
 MOE_API size_t moe_workspace_size_bwd(const moe_shape* s, int32_t S);
 
+/* The same for moe_balance_loss and moe_gate_bwd alone: the router's backward
+ * needs room for dlogits several times over. */
+MOE_API size_t moe_workspace_size_balance(const moe_shape* s, int32_t S);
+
 /* Balance loss and per-expert counts of a batch, in S sequences (or as one).
  *   logits      [T, E] fp32 in   moe_router's output
  *   idx         [T, k] int32 in  moe_topk's selections
@@ -480,7 +484,7 @@ MOE_API size_t moe_workspace_size_bwd(const moe_shape* s, int32_t S);
  *   tokens      [S+2] int32 out  counted tokens N_i of each sequence, then
  *               their sum N, then the number S' of sequences with N_i > 0
  *   prob_mean   [S, E] fp32 out or NULL   mean probability of each expert
- *   ws          moe_workspace_size_bwd(s, S) bytes
+ *   ws          moe_workspace_size_balance(s, S) bytes
  * A token counts if it lies in a sequence, its mask (if any) is not 0 and its
  * logits are not all -inf (single -inf logits are experts of probability 0).
  * With p the softmax of a token's logits and lse their logsumexp, over the

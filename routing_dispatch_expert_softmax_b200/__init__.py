@@ -17,7 +17,8 @@ from .binding import (EXPORTS, MOE_STAGE_EVENTS, STAGE_NAMES, MOE_ERR_CUDA, MOE_
                       moe_dispatch_dedup, moe_ffn_fp8, moe_forward_fp8,
                       moe_forward_fp8_staged, moe_ep_recv_experts, moe_ffn_w8a8,
                       moe_forward_w8a8, moe_forward_w8a8_staged, moe_quantise_rows_e4m3,
-                      moe_copy, moe_workspace_size_bwd, workspace_bwd, moe_balance_loss,
+                      moe_copy, moe_workspace_size_bwd, workspace_bwd,
+                      moe_workspace_size_balance, workspace_balance, moe_balance_loss,
                       moe_gate_bwd, moe_combine_bwd, moe_router_bwd, GradList, moe_grad_sumsq,
                       moe_grad_scale, moe_clip_grads)
 from .layer import MoELayer  # noqa: F401

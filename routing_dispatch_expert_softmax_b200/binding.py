@@ -37,7 +37,8 @@ EXPORTS = ("moe_error_string", "moe_version", "moe_workspace_size", "moe_router"
            "moe_workspace_size_eplb", "moe_forward_eplb", "moe_dispatch_dedup",
            "moe_ffn_fp8", "moe_forward_fp8", "moe_forward_fp8_staged", "moe_ep_recv_experts",
            "moe_ffn_w8a8", "moe_forward_w8a8", "moe_forward_w8a8_staged",
-           "moe_quantise_rows_e4m3", "moe_copy", "moe_workspace_size_bwd", "moe_balance_loss",
+           "moe_quantise_rows_e4m3", "moe_copy", "moe_workspace_size_bwd",
+           "moe_workspace_size_balance", "moe_balance_loss",
            "moe_gate_bwd", "moe_combine_bwd", "moe_router_bwd", "moe_workspace_size_grads",
            "moe_grad_sumsq", "moe_grad_scale", "moe_clip_grads")
 
@@ -146,6 +147,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     _f = ctypes.c_float
     lib.moe_workspace_size_bwd.restype = ctypes.c_size_t
     lib.moe_workspace_size_bwd.argtypes = [_S, _i32]
+    lib.moe_workspace_size_balance.restype = ctypes.c_size_t
+    lib.moe_workspace_size_balance.argtypes = [_S, _i32]
     lib.moe_balance_loss.restype = ctypes.c_int
     lib.moe_balance_loss.argtypes = [_P, _P, _P, _P, _i32, _S, _f, _f, _P, _P, _P, _P, _P, _P]
     lib.moe_gate_bwd.restype = ctypes.c_int
@@ -576,6 +579,11 @@ def _Operands(where):  # until the extension is loaded
 
 
 @functools.lru_cache(maxsize=1024)
+def _balance_bytes(T, d, E, k, f, R, S) -> int:
+    return moe_workspace_size_balance(MoEShape(T, d, E, k, f, R), S)
+
+
+@functools.lru_cache(maxsize=1024)
 def _bwd_bytes(T, d, E, k, f, R, S) -> int:
     return moe_workspace_size_bwd(MoEShape(T, d, E, k, f, R), S)
 
@@ -585,12 +593,26 @@ def moe_workspace_size_bwd(shape: MoEShape, S: int = 1) -> int:
 
 
 def workspace_bwd(shape: MoEShape, S: int = 1, device="cuda") -> torch.Tensor:
-    """A zeroed workspace for moe_balance_loss, moe_gate_bwd and
-    moe_router_bwd of this shape with up to S sequences."""
-    n = moe_workspace_size_bwd(shape, S)
+    """A workspace for moe_balance_loss, moe_gate_bwd and moe_router_bwd of this
+    shape with up to S sequences, its header zeroed."""
+    return _with_header(moe_workspace_size_bwd(shape, S), "moe_workspace_size_bwd", device)
+
+
+def moe_workspace_size_balance(shape: MoEShape, S: int = 1) -> int:
+    return int(load_library().moe_workspace_size_balance(ctypes.byref(shape), int(S)))
+
+
+def workspace_balance(shape: MoEShape, S: int = 1, device="cuda") -> torch.Tensor:
+    """The same for moe_balance_loss and moe_gate_bwd alone."""
+    return _with_header(moe_workspace_size_balance(shape, S), "moe_workspace_size_balance", device)
+
+
+def _with_header(n: int, where: str, device) -> torch.Tensor:
     if n == 0:
-        raise MoEError(MOE_ERR_INVALID_ARG, "moe_workspace_size_bwd")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+        raise MoEError(MOE_ERR_INVALID_ARG, where)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:64].zero_()
+    return ws
 
 
 def _seq_count(where, seq_offsets) -> int:
@@ -613,7 +635,7 @@ def moe_balance_loss(logits, idx, loss, counts, tokens, shape: MoEShape, ws, bal
     o = _Operands("moe_balance_loss")
     T, E, k = shape.T, shape.E, shape.k
     S = _seq_count(o.where, seq_offsets)
-    need = _bwd_bytes(T, shape.d, E, k, shape.f, shape.R, S)
+    need = _balance_bytes(T, shape.d, E, k, shape.f, shape.R, S)
     args = (o.ptr(logits, torch.float32, (T, E), "logits"),
             o.ptr(idx, torch.int32, (T, k), "idx"),
             o.ptr(token_mask, torch.uint8, (T,), "token_mask", True),

@@ -478,6 +478,11 @@ size_t moe_workspace_size_bwd(const moe_shape* s, int32_t S) {
   return bwd_bytes(*s, S);
 }
 
+size_t moe_workspace_size_balance(const moe_shape* s, int32_t S) {
+  if (!shape_ok(s) || S < 1 || S > kMaxSeqs) return 0;
+  return bwd_layout(*s, S).balance;
+}
+
 int moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* token_mask,
                      const int32_t* seq_offsets, int32_t S, const moe_shape* s,
                      float balance_coef, float z_coef, float* loss, int32_t* counts,

@@ -28,7 +28,7 @@ struct BwdLayout {
   // gradients of the token ranges
   int cp, plane_rows;
   size_t dl_planes, dl_half, w_half, dl_back, w_back, db_part, dw_part;
-  size_t rest;  // the bytes of all but dw_part
+  size_t balance, rest;  // the bytes for the balance loss, and of all but dw_part
 };
 
 // How the router's backward lays dL's three bf16 planes out for dW's 128-row MMA
@@ -119,7 +119,7 @@ inline BwdLayout bwd_layout(const moe_shape& s, int S) {
   L.n = take(sizeof(int) * slots);
   L.term = take(sizeof(double) * (size_t)S * ((E + 31) / 32));
   L.zterm = take(sizeof(double) * S);
-  const size_t balance = o;
+  L.balance = o;
   o = 256;
   L.cp = (int)align_up(E, 64);
   // up to 64 tokens one block, whose column sums need no second kernel
@@ -132,7 +132,7 @@ inline BwdLayout bwd_layout(const moe_shape& s, int S) {
   L.w_back = take(2 * (size_t)d);
   L.db_part = take(sizeof(float) * (size_t)((T + L.plane_rows - 1) / L.plane_rows) * E);
   L.dw_part = o;
-  L.rest = std::max(balance, o);
+  L.rest = std::max(L.balance, o);
   return L;
 }
 
