@@ -624,6 +624,11 @@ def _seq_count(where, seq_offsets) -> int:
     return seq_offsets.numel() - 1
 
 
+def _as_bytes(mask):
+    """A bool mask's own bytes; anything else as it is."""
+    return mask.view(torch.uint8) if getattr(mask, "dtype", None) is torch.bool else mask
+
+
 def moe_balance_loss(logits, idx, loss, counts, tokens, shape: MoEShape, ws, balance_coef=1e-2,
                      z_coef=0.0, token_mask=None, seq_offsets=None, prob_mean=None, stream=None):
     """Balance and z loss with per-expert counts, over the S sequences of
@@ -631,14 +636,14 @@ def moe_balance_loss(logits, idx, loss, counts, tokens, shape: MoEShape, ws, bal
     (S = 1).  ``loss`` (3,) receives {balance + z, balance, z}, ``counts``
     (S, E) and ``tokens`` (S + 2,) what moe_gate_bwd reads again,
     ``prob_mean`` (S, E), if given, the experts' mean probabilities.
-    ``token_mask`` (T,) uint8: 0 leaves the token out."""
+    ``token_mask`` (T,) bool or uint8: 0 leaves the token out."""
     o = _Operands("moe_balance_loss")
     T, E, k = shape.T, shape.E, shape.k
     S = _seq_count(o.where, seq_offsets)
     need = _balance_bytes(T, shape.d, E, k, shape.f, shape.R, S)
     args = (o.ptr(logits, torch.float32, (T, E), "logits"),
             o.ptr(idx, torch.int32, (T, k), "idx"),
-            o.ptr(token_mask, torch.uint8, (T,), "token_mask", True),
+            o.ptr(_as_bytes(token_mask), torch.uint8, (T,), "token_mask", True),
             o.ptr(seq_offsets, torch.int32, None, "seq_offsets", True), S, ctypes.byref(shape),
             balance_coef, z_coef, o.ptr(loss, torch.float32, (3,), "loss"),
             o.ptr(counts, torch.int32, (S, E), "counts"),
@@ -662,7 +667,7 @@ def moe_gate_bwd(logits, idx, dlogits, shape: MoEShape, ws, w=None, dw=None, cou
             o.ptr(idx, torch.int32, (T, k), "idx", not gates),
             o.ptr(w, torch.float32, (T, k), "w", not gates),
             o.ptr(dw, torch.float32, (T, k), "dw", True),
-            o.ptr(token_mask, torch.uint8, (T,), "token_mask", True),
+            o.ptr(_as_bytes(token_mask), torch.uint8, (T,), "token_mask", True),
             o.ptr(seq_offsets, torch.int32, None, "seq_offsets", True), S,
             o.ptr(counts, torch.int32, (S, E), "counts", True),
             o.ptr(tokens, torch.int32, (S + 2,), "tokens", not aux), ctypes.byref(shape),

@@ -78,3 +78,22 @@ def test_a_prerelease_torch_has_an_extension_too():
 def test_the_built_extension_names_the_whole_version():
     B.load_library()
     assert B._native.TORCH == str(torch.__version__)
+
+
+def test_a_bool_token_mask_is_checked_like_another():
+    run("import torch\n"
+        "import routing_dispatch_expert_softmax_b200 as moe\n"
+        "from routing_dispatch_expert_softmax_b200 import binding as B\n"
+        "moe.load_library()\n"
+        "class O(B._native.Operands):\n"
+        "    def ptr(self, t, dtype, shape, name, optional=False):\n"
+        "        if name == 'token_mask': raise KeyError(t.dtype, dtype)\n"
+        "        return 0\n"
+        "B._Operands = O\n"
+        "s = moe.MoEShape.of(4, 64, 8, 2, 64)\n"
+        "for call in (lambda m: moe.moe_balance_loss(0, 0, 0, 0, 0, s, None, token_mask=m),\n"
+        "             lambda m: moe.moe_gate_bwd(0, 0, 0, s, None, token_mask=m)):\n"
+        "    for m, seen in ((torch.ones(4, dtype=torch.bool), torch.uint8), (torch.ones(4), torch.float32)):\n"
+        "        try: call(m)\n"
+        "        except KeyError as e: assert e.args == (seen, torch.uint8), e.args\n"
+        "        else: assert False\n")
