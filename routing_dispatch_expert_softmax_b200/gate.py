@@ -24,7 +24,7 @@ class GateGrads(NamedTuple):
     dbias: Optional[torch.Tensor]     # (E,) fp32, for a layer with a bias
     dx: Optional[torch.Tensor]        # (T, d) bf16: x's gradient through the gate alone
     dz: Optional[torch.Tensor]        # (T*k, d) bf16: the experts' output rows'
-    norm: Optional[torch.Tensor]      # (1,) fp32: of dw_g and dbias, before clipping
+    norm: Optional[torch.Tensor]      # (1,) fp32: of this layer's dw_g and dbias, before clipping
 
 
 class GateTrainer:
@@ -114,8 +114,10 @@ class GateTrainer:
                  max_norm: Optional[float] = None) -> GateGrads:
         """Gradients for the loss whose gradient on y is ``dy`` (T, d) bf16,
         plus ``dloss`` (a (1,) fp32 device tensor, default 1) times the
-        balance loss.  ``max_norm``: clips dw_g and dbias by their global
-        norm."""
+        balance loss.  ``max_norm``: clips this layer's dw_g and dbias by the norm
+        of the two.  For the norm over several layers leave it out and give their
+        gradients to one moe_clip_grads.  ``dx`` and ``dz`` end here: the experts'
+        own backward, and with it x's gradient through them, is the caller's."""
         if self._kept is None:
             raise RuntimeError("backward needs a forward first")
         q, layer = self._kept, self.layer

@@ -120,3 +120,22 @@ def test_two_captures_of_one_trainer_beside_each_other(made):
     for (_, out), w in zip(made_graphs, want):
         assert same(out, w)
     assert same(step(tr, xs[1], dy, seqs), want[1])
+
+
+def test_clipping_several_layers_by_one_norm(made):
+    cfg, t, layer = made
+    dy = torch.randn(300, cfg.d, device=DEV).bfloat16()
+    grads = []
+    for seed in range(3):
+        u = wl.make_layer(cfg, DEV, 10 + seed)
+        tr = moe.GateTrainer(moe.MoELayer(u["w_g"], u["bias"], u["w13"], u["w2"], cfg.k))
+        tr(u["x"])
+        g = tr.backward(dy)
+        grads += [v for v in (g.dw_g, g.dbias) if v is not None]
+    whole = [g.clone() for g in grads]
+    norm = torch.empty(1, device=DEV)
+    moe.moe_clip_grads(grads, 0.25, norm)
+    want = sum(float(g.double().square().sum()) for g in whole) ** 0.5
+    assert want > 0.25 and abs(norm.item() - want) <= 1e-6 * want
+    for g, w in zip(grads, whole):
+        assert torch.allclose(g.double(), w.double() * (0.25 / (want + 1e-6)), rtol=1e-6, atol=0)
