@@ -20,7 +20,7 @@ namespace {
 constexpr int kUnit = 2048;       // elements
 constexpr int kPiece = 32;        // most units of a block's run in one round
 // Tensors of one launch.  A table is copied with the launch, so a short list takes a
-// small one (2 or 8 KB); the largest has 24 of the 32 KB of a launch's parameters.
+// small one (2.5 or 10 KB); the largest has 30 of the 32 KB of a launch's parameters.
 constexpr int kTables[3] = {64, 256, 768};
 constexpr int kGradBlocks = 592;  // blocks of one launch (partial sums), 4 for each SM
 
