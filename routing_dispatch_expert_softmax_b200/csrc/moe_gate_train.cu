@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(256, RowCfg<LPR, NV, VEC>::kBlocks) k_balance_
   bool bad_id = false;
   while (t < t1 && s < S) {
     const int end = off ? min(t1, __ldg(off + s + 1)) : t1;
-    if (end <= t) {  // an empty sequence
-      ++s;
+    if (end <= t) {  // an empty sequence, perhaps the first of thousands (a step each: 7 ms)
+      s = max(s + 1, find_seq(off, S, t));
       continue;
     }
     f32x2 acc[NV / 2];
