@@ -495,7 +495,8 @@ MOE_API size_t moe_workspace_size_balance(const moe_shape* s, int32_t S);
  * out).  NaN or +inf in a counted token's logits makes its sequence's results
  * NaN; uncounted tokens' values are not looked at.  Bad offsets and ids
  * outside [0, E) are recorded as MOE_ERR_DEVICE_CHECK; such an id is not
- * counted. */
+ * counted.  p and lse^2 are fp32 and summed in fp32 over a block's tokens
+ * (T / 296 + 32 at most), the blocks' sums in fp64. */
 MOE_API int moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* token_mask,
                              const int32_t* seq_offsets, int32_t S, const moe_shape* s,
                              float balance_coef, float z_coef, float* loss, int32_t* counts,
@@ -547,8 +548,9 @@ MOE_API int moe_combine_bwd(const moe_bf16* dy, const moe_bf16* z, const int32_t
  * and a term is off by 2^-19 of itself at most: with few tokens tf32 parts (a value may
  * also lose 2^-137), else fp16 ones (rows scaled by powers of two; a value may also
  * lose 2^-38 of its row's largest).
- * Where x, dlogits or w_g are not finite, so are the results
- * they reach (NaN in place of some infinities).
+ * dbias: fp32 sums of up to 192 tokens or of a block's (T / 592 + 32), those in fp64.
+ * Where x, dlogits or w_g are not finite, so are the results they reach (NaN in place
+ * of some infinities).
  *   ws moe_workspace_size_bwd(s, 1) bytes */
 MOE_API int moe_router_bwd(const moe_bf16* x, const float* w_g, const float* dlogits,
                            const moe_shape* s, float* dw_g, float* dbias, moe_bf16* dx, void* ws,

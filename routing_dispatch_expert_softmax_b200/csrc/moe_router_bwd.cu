@@ -71,7 +71,8 @@ __device__ __forceinline__ void half_scale(float top, float& scale, float& back)
 //   half [rows][2][cp], back [rows]  its rows scaled, in two fp16 parts (rounded, and
 //                         the rounded rest), cp = cols rounded up to 64 with zeros,
 //                         and the square roots of the factors that undo the scaling
-//   sums [block][cols]    column sums of each block's rows
+//   sums [block][cols]    column sums of each block's rows, in fp32 (T / 592 + 32 rows
+//                         at most, each thread a few of them; the blocks' go into fp64)
 struct PlanesArgs {
   const float* a;
   __nv_bfloat16* planes;
@@ -917,7 +918,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps, KS <= 4 ? 2 : 1)
       *reinterpret_cast<uint32_t*>(a.dx + (size_t)t * a.d + i0 + i) = pack_bf16x2(s0, s1);
     }
   }
-  if (a.db)  // each block some experts
+  if (a.db)  // each block some experts; up to 192 values, off by 2^-17 of their sum at most
     for (int e = blockIdx.x * blockDim.x + threadIdx.x; e < a.E; e += gridDim.x * blockDim.x) {
       float s = 0.f;
 #pragma unroll 8
