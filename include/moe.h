@@ -496,7 +496,7 @@ MOE_API size_t moe_workspace_size_balance(const moe_shape* s, int32_t S);
  * NaN; uncounted tokens' values are not looked at.  Bad offsets and ids
  * outside [0, E) are recorded as MOE_ERR_DEVICE_CHECK; such an id is not
  * counted.  p and lse^2 are fp32 and summed in fp32 over a block's tokens
- * (T / 296 + 32 at most), the blocks' sums in fp64. */
+ * (T / 296 + 64 at most), the blocks' sums in fp64. */
 MOE_API int moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* token_mask,
                              const int32_t* seq_offsets, int32_t S, const moe_shape* s,
                              float balance_coef, float z_coef, float* loss, int32_t* counts,

@@ -918,7 +918,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps, KS <= 4 ? 2 : 1)
       *reinterpret_cast<uint32_t*>(a.dx + (size_t)t * a.d + i0 + i) = pack_bf16x2(s0, s1);
     }
   }
-  if (a.db)  // each block some experts; up to 192 values, off by 2^-17 of their sum at most
+  if (a.db)  // each block some experts; up to 192 values, 2^-24 an add
     for (int e = blockIdx.x * blockDim.x + threadIdx.x; e < a.E; e += gridDim.x * blockDim.x) {
       float s = 0.f;
 #pragma unroll 8
