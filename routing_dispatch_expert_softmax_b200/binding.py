@@ -3,10 +3,10 @@
 Argument marshalling only (the checks of the calls that train the gate
 natively, in ``_operands.so``, which the others do without): every step of the
 layer runs in the library's CUDA kernels.  Tensors are torch CUDA tensors
-(PyTorch supplies device memory and streams; the layer calls' y and moe_copy's operands may also be pinned host
-tensors); the functions keep the C names and raise :class:`MoEError` on a
-non-zero status.  There is no fallback: if the library is missing or the
-device is not an sm_100 GPU, calls raise.
+(PyTorch supplies device memory and streams; the layer calls' y and moe_copy's
+operands may also be pinned host tensors); the functions keep the C names and
+raise :class:`MoEError` on a non-zero status.  There is no fallback: if the
+library is missing or the device is not an sm_100 GPU, calls raise.
 """
 
 from __future__ import annotations

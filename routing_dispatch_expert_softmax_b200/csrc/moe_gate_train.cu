@@ -23,8 +23,8 @@ namespace {
 // (reductions, the k slots), so a lane holds 8 values up to 256 experts and a warp
 // takes 32 / LPR rows at once: with 4 values (two rows of 64 experts a warp in place
 // of four, one of 128 in place of two) the gate's gradient of 131072 rows took 29
-// and 49 us in place of 21 and 36 (18 and 34 since).  Above 256 experts a warp has one row.  The next
-// rows' loads are in flight meanwhile, up to 512 experts.
+// and 49 us in place of 21 and 36 (18 and 34 since).  Above 256 experts a warp has one
+// row.  The next rows' loads are in flight meanwhile, up to 512 experts.
 template <int LPR, int NV, bool VEC>
 struct RowCfg {
   static constexpr int kLpr = LPR, kNv = NV;

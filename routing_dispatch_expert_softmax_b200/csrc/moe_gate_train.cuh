@@ -22,10 +22,10 @@ struct BwdLayout {
   // pair that meets (at most blocks + S of them)
   int chunk;
   size_t prob, count, z, n, term, zterm;
-  // router backward: bf16 planes of dlogits (router_planes), dlogits [T][2][cp] and
-  // w_g [d][2][cp] in two fp16 parts (cp = E rounded up to 64) with the roots of the factors that undo
-  // their rows' scaling, column sums of every plane_rows tokens, and (last) partial weight
-  // gradients of the token ranges
+  // router backward: bf16 planes of dlogits (router_planes), dlogits [T][2][cp] and w_g
+  // [d][2][cp] in two fp16 parts (cp = E rounded up to 64) with the roots of the factors
+  // that undo their rows' scaling, column sums of every plane_rows tokens, and (last)
+  // partial weight gradients of the token ranges
   int cp, plane_rows;
   size_t dl_planes, dl_half, w_half, dl_back, w_back, db_part, dw_part;
   size_t balance, rest;  // the bytes for the balance loss, and of all but dw_part
