@@ -718,7 +718,8 @@ class GradList:
     another gradient or out.  The tensors are looked at again at every call: what
     they have become (their ``.data`` replaced) is what is scaled, or refused.
     As with any workspace, calls on one GradList must not run concurrently, and
-    come after its making in stream order."""
+    come after its making in stream order; one made under capture is that
+    graph's."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
